@@ -373,3 +373,8 @@ def q8_0_debug_read_lds(seen: torch.Tensor, workgroups: int) -> None:
     assert seen.numel() * seen.element_size() >= workgroups * DEBUG_LDS_DWORDS * 4
     _check(_lib.q8_0_debug_read_lds(_dev(seen, "seen"), int(workgroups), _stream()),
            "q8_0_debug_read_lds")
+
+
+# The MXFP4 operators and the MoE router (include/mxfp4.h).
+from .mxfp4 import (MXFP4_BF16, MXFP4_BLOCK_ELEMS, MXFP4_F16, MXFP4_F32, Mxfp4,  # noqa: E402
+                    mxfp4_dequantize, mxfp4_quantize)

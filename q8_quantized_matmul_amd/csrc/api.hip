@@ -17,26 +17,11 @@ static_assert(Q8_0_MOE_STATIC_SCRATCH_BYTES == q8::kMoeStaticScratchBytes,
 static_assert(Q8_0_DEBUG_LDS_DWORDS == q8::kDebugLdsDwords,
               "header and library agree on the LDS read-back size");
 
-namespace {
-
-// Regimes by token count (measured on 4096->2048, 2048->4096, 4096->1024,
-// 4096->512 and 1024->32768, graph-replayed calls): the weight-streaming
-// matvec below 12 tokens, the skinny matrix-core kernel (one launch, split-K
-// inside it) from 12 to 64 and, for shapes skinny_many_tokens accepts, up to
-// 256; the LDS-tiled GEMM above.  Rows the matvec
-// cannot take (pair counts that are neither a power of two below 64 nor a
-// multiple of 64, e.g. in_dim 1536 or 7168) go to the skinny kernel from two
-// tokens: the generic kernel's cost grows by 3-4 us per token there.
-constexpr int64_t kSkinnyMinTokens = 12;
-// The shared list launch takes the matvec items, so below the skinny regime.
-constexpr int64_t kListMaxTokens = kSkinnyMinTokens - 1;
-constexpr int32_t kMaxExperts = 8192;
-constexpr int kMaxDevices = 64;
+namespace q8 {
 
 // 1 = gfx950, -1 = other architecture, 0 = not looked at yet.
-std::atomic<int> g_device_ok[kMaxDevices];
-
-bool aligned(const void *p, uintptr_t a) { return (reinterpret_cast<uintptr_t>(p) & (a - 1)) == 0; }
+static constexpr int kMaxDevices = 64;
+static std::atomic<int> g_device_ok[kMaxDevices];
 
 int check_device() {
   int dev = 0;
@@ -50,6 +35,27 @@ int check_device() {
   }
   return state == 1 ? Q8_0_OK : Q8_0_ENODEV;
 }
+
+}  // namespace q8
+
+namespace {
+
+using q8::check_device;
+
+// Regimes by token count (measured on 4096->2048, 2048->4096, 4096->1024,
+// 4096->512 and 1024->32768, graph-replayed calls): the weight-streaming
+// matvec below 12 tokens, the skinny matrix-core kernel (one launch, split-K
+// inside it) from 12 to 64 and, for shapes skinny_many_tokens accepts, up to
+// 256; the LDS-tiled GEMM above.  Rows the matvec
+// cannot take (pair counts that are neither a power of two below 64 nor a
+// multiple of 64, e.g. in_dim 1536 or 7168) go to the skinny kernel from two
+// tokens: the generic kernel's cost grows by 3-4 us per token there.
+constexpr int64_t kSkinnyMinTokens = 12;
+// The shared list launch takes the matvec items, so below the skinny regime.
+constexpr int64_t kListMaxTokens = kSkinnyMinTokens - 1;
+constexpr int32_t kMaxExperts = 8192;
+
+bool aligned(const void *p, uintptr_t a) { return (reinterpret_cast<uintptr_t>(p) & (a - 1)) == 0; }
 
 int status_of(hipError_t e) { return e == hipSuccess ? Q8_0_OK : Q8_0_ELAUNCH; }
 

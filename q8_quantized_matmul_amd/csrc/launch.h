@@ -1,11 +1,14 @@
 // launch.h -- internal host-side launchers, one per kernel family.  Each
-// returns hipSuccess or the launch error; argument checks happen in api.cpp.
+// returns hipSuccess or the launch error; argument checks happen in api.hip.
 #pragma once
 
 #include <hip/hip_runtime.h>
 #include <stdint.h>
 
 namespace q8 {
+
+// api.hip: Q8_0_OK if the current device is a gfx950, Q8_0_ENODEV otherwise.
+int check_device();
 
 // quantize.hip
 hipError_t launch_quantize(void *x_q, const float *x, int64_t n_tok, int64_t in_dim,

@@ -1,0 +1,59 @@
+// mxfp4_api.hip -- the C ABI of include/mxfp4.h: host-side argument checks and
+// launches on the caller's stream.  Nothing here allocates device memory.
+#include <stdint.h>
+
+#include "launch.h"
+#include "mxfp4.h"
+#include "mxfp4_launch.h"
+
+static_assert(MXFP4_F32 == mx::kF32 && MXFP4_BF16 == mx::kBF16 && MXFP4_F16 == mx::kF16,
+              "header and library agree on the element types");
+
+namespace {
+
+bool aligned(const void *p, uintptr_t a) { return (reinterpret_cast<uintptr_t>(p) & (a - 1)) == 0; }
+bool type_ok(int32_t t) { return t == MXFP4_F32 || t == MXFP4_BF16 || t == MXFP4_F16; }
+int type_size(int32_t t) { return t == MXFP4_F32 ? 4 : 2; }
+int status_of(hipError_t e) { return e == hipSuccess ? Q8_0_OK : Q8_0_ELAUNCH; }
+
+// A grid has fewer than 2^31 workgroups of 8192 values: the largest matrix the
+// elementwise kernels take.
+constexpr int64_t kMaxElems = int64_t{1} << 43;
+
+// Sizes of a matrix that a call reads or writes: Q8_0_OK, or EINVAL.
+int check_matrix(int64_t rows, int64_t k) {
+  if (rows < 0 || k < 0 || k % MXFP4_BLOCK_ELEMS != 0) return Q8_0_EINVAL;
+  if (k > 0 && rows > kMaxElems / k) return Q8_0_EINVAL;
+  return Q8_0_OK;
+}
+
+}  // namespace
+
+extern "C" {
+
+int mxfp4_quantize(void *codes, void *scales, const void *x, int32_t x_type, int64_t x_stride,
+                   int64_t n_rows, int64_t in_dim, hipStream_t stream) {
+  int st = check_matrix(n_rows, in_dim);
+  if (st != Q8_0_OK || !type_ok(x_type) || x_stride < in_dim) return Q8_0_EINVAL;
+  if (n_rows == 0 || in_dim == 0) return Q8_0_OK;
+  if (!codes || !scales || !x) return Q8_0_EINVAL;
+  if (!aligned(codes, 16) || !aligned(x, type_size(x_type))) return Q8_0_EALIGN;
+  if ((st = q8::check_device()) != Q8_0_OK) return st;
+  return status_of(mx::launch_quantize(static_cast<uint8_t *>(codes), static_cast<uint8_t *>(scales),
+                                       x, x_type, x_stride, n_rows, in_dim, stream));
+}
+
+int mxfp4_dequantize(void *out, int32_t out_type, const void *codes, const void *scales,
+                     int64_t n_rows, int64_t in_dim, hipStream_t stream) {
+  int st = check_matrix(n_rows, in_dim);
+  if (st != Q8_0_OK || !type_ok(out_type)) return Q8_0_EINVAL;
+  if (n_rows == 0 || in_dim == 0) return Q8_0_OK;
+  if (!out || !codes || !scales) return Q8_0_EINVAL;
+  if (!aligned(codes, 16) || !aligned(out, 16)) return Q8_0_EALIGN;
+  if ((st = q8::check_device()) != Q8_0_OK) return st;
+  return status_of(mx::launch_dequantize(out, out_type, static_cast<const uint8_t *>(codes),
+                                         static_cast<const uint8_t *>(scales), n_rows, in_dim,
+                                         stream));
+}
+
+}  // extern "C"

@@ -1,0 +1,19 @@
+// mxfp4_launch.h -- internal host-side launchers of the MXFP4 operators.  Each
+// returns hipSuccess or the launch error; argument checks happen in
+// mxfp4_api.hip.
+#pragma once
+
+#include <hip/hip_runtime.h>
+#include <stdint.h>
+
+namespace mx {
+
+constexpr int kF32 = 0, kBF16 = 1, kF16 = 2;  // MXFP4_F32, MXFP4_BF16, MXFP4_F16
+
+// mxfp4_quantize.hip
+hipError_t launch_quantize(uint8_t *codes, uint8_t *scales, const void *x, int x_type,
+                           int64_t x_stride, int64_t n_rows, int64_t in_dim, hipStream_t s);
+hipError_t launch_dequantize(void *out, int out_type, const uint8_t *codes, const uint8_t *scales,
+                             int64_t n_rows, int64_t in_dim, hipStream_t s);
+
+}  // namespace mx
