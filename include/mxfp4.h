@@ -59,6 +59,41 @@ int mxfp4_quantize(void *codes, void *scales, const void *x, int32_t x_type, int
 int mxfp4_dequantize(void *out, int32_t out_type, const void *codes, const void *scales,
                      int64_t n_rows, int64_t in_dim, hipStream_t stream);
 
+/* Scores of moe_topk, from a token's logits z. */
+enum {
+    MOE_SOFTMAX = 0,      /* exp(z) / sum exp(z); ordered by z itself */
+    MOE_SIGMOID = 1,      /* 1 / (1 + exp(-z))                       */
+    MOE_SQRT_SOFTPLUS = 2 /* sqrt(log(1 + exp(z)))                   */
+};
+
+#define MOE_MAX_EXPERTS 1024
+#define MOE_MAX_USED 32
+
+/* The router: each token's n_used experts of largest score + bias, largest
+ * first, ties to the lowest id, with their weights.  Its outputs are the
+ * `selected` and `weights` of q8_0_moe_ffn and q8_0_moe_grouped.
+ *   selected : int32 [n_tok][n_used], written.
+ *   weights  : fp32 [n_tok][n_used], written: the scores (without bias) of the
+ *              chosen experts, divided by their sum if renormalize is set (for
+ *              MOE_SOFTMAX without it, by the sum over all experts), times `scale`
+ *              (a sum of exactly zero divides nothing: those weights are 0).
+ *   logits   : fp32 [n_tok][n_expert] (a router projection's output).
+ *   bias     : fp32 [n_expert] added to the score for the choice only (to the
+ *              logit for MOE_SOFTMAX), or NULL.
+ * An expert whose logit or biased score is -infinity is never chosen: a token
+ * with fewer than n_used others gets id -1 and weight 0 in its last slots (all
+ * of them for a token whose logits are all -infinity, e.g. padding).  NaN keys
+ * come before all others, and a NaN or +infinite score among those summed
+ * makes the weights that its sum divides NaN.
+ * MOE_SOFTMAX compares z + bias in fp32; the other scores are formed and
+ * compared in 64 bits.
+ * Errors: n_expert outside [1, MOE_MAX_EXPERTS], n_used outside [1,
+ * min(n_expert, MOE_MAX_USED)], n_tok * n_used above 2^31 - 1, unknown scoring,
+ * null pointers -> Q8_0_EINVAL; pointers not 4-byte aligned -> Q8_0_EALIGN. */
+int moe_topk(int32_t *selected, float *weights, const float *logits, const float *bias,
+             int64_t n_tok, int32_t n_expert, int32_t n_used, int32_t scoring,
+             int32_t renormalize, float scale, hipStream_t stream);
+
 #ifdef __cplusplus
 }
 #endif

@@ -376,5 +376,6 @@ def q8_0_debug_read_lds(seen: torch.Tensor, workgroups: int) -> None:
 
 
 # The MXFP4 operators and the MoE router (include/mxfp4.h).
-from .mxfp4 import (MXFP4_BF16, MXFP4_BLOCK_ELEMS, MXFP4_F16, MXFP4_F32, Mxfp4,  # noqa: E402
-                    mxfp4_dequantize, mxfp4_quantize)
+from .mxfp4 import (MOE_SIGMOID, MOE_SOFTMAX, MOE_SQRT_SOFTPLUS, MXFP4_BF16,  # noqa: E402
+                    MXFP4_BLOCK_ELEMS, MXFP4_F16, MXFP4_F32, Mxfp4, moe_topk, mxfp4_dequantize,
+                    mxfp4_quantize)

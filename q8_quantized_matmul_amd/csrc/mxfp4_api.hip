@@ -3,11 +3,16 @@
 #include <stdint.h>
 
 #include "launch.h"
+#include "moe_topk.h"
 #include "mxfp4.h"
 #include "mxfp4_launch.h"
 
 static_assert(MXFP4_F32 == mx::kF32 && MXFP4_BF16 == mx::kBF16 && MXFP4_F16 == mx::kF16,
               "header and library agree on the element types");
+static_assert(MOE_SOFTMAX == mx::kSoftmax && MOE_SIGMOID == mx::kSigmoid &&
+                  MOE_SQRT_SOFTPLUS == mx::kSqrtSoftplus &&
+                  MOE_MAX_EXPERTS == mx::kMaxRouteExperts && MOE_MAX_USED == mx::kMaxUsed,
+              "header and library agree on the router");
 
 namespace {
 
@@ -24,6 +29,18 @@ constexpr int64_t kMaxElems = int64_t{1} << 43;
 int check_matrix(int64_t rows, int64_t k) {
   if (rows < 0 || k < 0 || k % MXFP4_BLOCK_ELEMS != 0) return Q8_0_EINVAL;
   if (k > 0 && rows > kMaxElems / k) return Q8_0_EINVAL;
+  return Q8_0_OK;
+}
+
+int check_route(const float *logits, const float *bias, int64_t n_tok, int32_t n_expert,
+                int32_t n_used, int32_t scoring) {
+  if (n_tok < 0 || n_expert < 1 || n_expert > MOE_MAX_EXPERTS || n_used < 1 || n_used > n_expert ||
+      n_used > MOE_MAX_USED || scoring < MOE_SOFTMAX || scoring > MOE_SQRT_SOFTPLUS)
+    return Q8_0_EINVAL;
+  if (n_tok > INT32_MAX / n_used) return Q8_0_EINVAL;
+  if (n_tok == 0) return Q8_0_OK;
+  if (!logits) return Q8_0_EINVAL;
+  if (!aligned(logits, 4) || !aligned(bias, 4)) return Q8_0_EALIGN;
   return Q8_0_OK;
 }
 
@@ -54,6 +71,18 @@ int mxfp4_dequantize(void *out, int32_t out_type, const void *codes, const void 
   return status_of(mx::launch_dequantize(out, out_type, static_cast<const uint8_t *>(codes),
                                          static_cast<const uint8_t *>(scales), n_rows, in_dim,
                                          stream));
+}
+
+int moe_topk(int32_t *selected, float *weights, const float *logits, const float *bias,
+             int64_t n_tok, int32_t n_expert, int32_t n_used, int32_t scoring,
+             int32_t renormalize, float scale, hipStream_t stream) {
+  int st = check_route(logits, bias, n_tok, n_expert, n_used, scoring);
+  if (st != Q8_0_OK || n_tok == 0) return st;
+  if (!selected || !weights) return Q8_0_EINVAL;
+  if (!aligned(selected, 4) || !aligned(weights, 4)) return Q8_0_EALIGN;
+  if ((st = q8::check_device()) != Q8_0_OK) return st;
+  const mx::RouteArgs a{logits, bias, n_expert, n_used, scoring, renormalize != 0, scale};
+  return status_of(mx::launch_topk(a, n_tok, selected, weights, stream));
 }
 
 }  // extern "C"

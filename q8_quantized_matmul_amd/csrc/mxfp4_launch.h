@@ -16,4 +16,9 @@ hipError_t launch_quantize(uint8_t *codes, uint8_t *scales, const void *x, int x
 hipError_t launch_dequantize(void *out, int out_type, const uint8_t *codes, const uint8_t *scales,
                              int64_t n_rows, int64_t in_dim, hipStream_t s);
 
+// moe_topk.hip
+struct RouteArgs;
+hipError_t launch_topk(const RouteArgs &a, int64_t n_tok, int32_t *selected, float *weights,
+                       hipStream_t s);
+
 }  // namespace mx

@@ -17,11 +17,14 @@ from . import Q8Error, _i32, _i64, _lib, _sz, _vp
 
 MXFP4_BLOCK_ELEMS = 32
 MXFP4_F32, MXFP4_BF16, MXFP4_F16 = 0, 1, 2
+MOE_SOFTMAX, MOE_SIGMOID, MOE_SQRT_SOFTPLUS = 0, 1, 2
 _TYPES = {torch.float32: MXFP4_F32, torch.bfloat16: MXFP4_BF16, torch.float16: MXFP4_F16}
 
 _sig = {
     "mxfp4_quantize": ([_vp, _vp, _vp, _i32, _i64, _i64, _i64, _vp], ctypes.c_int),
     "mxfp4_dequantize": ([_vp, _i32, _vp, _vp, _i64, _i64, _vp], ctypes.c_int),
+    "moe_topk": ([_vp, _vp, _vp, _vp, _i64, _i32, _i32, _i32, _i32, ctypes.c_float, _vp],
+                 ctypes.c_int),
 }
 for _name, (_args, _res) in _sig.items():
     _fn = getattr(_lib, _name)
@@ -126,3 +129,29 @@ def mxfp4_dequantize(m: Mxfp4, dtype: torch.dtype = torch.float32,
     _run("mxfp4_dequantize", device, _ptr(out, "out", out.dtype, device), _type(out.dtype, "out"),
          c, s, lead.numel(), k)
     return out
+
+
+def moe_topk(logits: torch.Tensor, n_used: int, bias: torch.Tensor = None,
+             scoring: int = MOE_SOFTMAX, renormalize: bool = True, scale: float = 1.0,
+             selected: torch.Tensor = None, weights: torch.Tensor = None):
+    """(selected int32, weights float32), both [n_tok][n_used]: each token's experts of
+    largest score + bias from float32 logits [n_tok][n_expert].  Slots without an
+    eligible expert (logits of -inf) hold id -1 and weight 0."""
+    if logits.dim() != 2:
+        raise ValueError("logits must be [n_tok][n_expert]")
+    device = _device(logits, "logits")
+    n_tok, n_expert = logits.shape
+    if selected is None:
+        selected = torch.empty((n_tok, n_used), dtype=torch.int32, device=device)
+    if weights is None:
+        weights = torch.empty((n_tok, n_used), dtype=torch.float32, device=device)
+    _shape(selected, "selected", n_tok, n_used)
+    _shape(weights, "weights", n_tok, n_used)
+    if bias is not None:
+        _shape(bias, "bias", n_expert)
+        bias = _ptr(bias, "bias", torch.float32, device)
+    _run("moe_topk", device, _ptr(selected, "selected", torch.int32, device),
+         _ptr(weights, "weights", torch.float32, device),
+         _ptr(logits, "logits", torch.float32, device), bias, n_tok, n_expert, n_used, scoring,
+         int(renormalize), scale)
+    return selected, weights

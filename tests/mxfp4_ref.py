@@ -53,3 +53,36 @@ def device(q8, m):
 def host(t):
     """float64 numpy values of a device tensor."""
     return t.detach().cpu().double().numpy()
+
+
+def route(logits, n_used, bias=None, scoring=0, renormalize=True, scale=1.0):
+    """(ids int32, weights float64) of float32 logits [t][e]: 0 softmax, 1 sigmoid,
+    2 sqrt(softplus).  Softmax keys are fp32 sums, the others float64."""
+    z32 = np.asarray(logits, dtype=np.float32)
+    z = z32.astype(np.float64)
+    t, e = z.shape
+    with np.errstate(all="ignore"):
+        if scoring == 0:
+            score = z
+            key = z if bias is None else (z32 + np.asarray(bias, np.float32)).astype(np.float64)
+        else:
+            score = 1 / (1 + np.exp(-z)) if scoring == 1 else np.sqrt(np.log1p(np.exp(-np.abs(z))) + np.maximum(z, 0))
+            key = score if bias is None else score + np.asarray(bias, np.float64)
+        key = np.where(np.isneginf(z), -np.inf, key)
+        rank = np.where(np.isnan(key), np.inf, key)
+        second = np.where(np.isnan(key), 0, 1)          # NaN before +inf
+        ids = np.full((t, n_used), -1, dtype=np.int32)
+        w = np.zeros((t, n_used))
+        for r in range(t):
+            order = sorted(range(e), key=lambda i: (-rank[r, i], second[r, i], i))
+            chosen = [i for i in order if not np.isneginf(key[r, i])][:n_used]
+            ids[r, :len(chosen)] = chosen
+            s = score[r, chosen]
+            if scoring == 0 and chosen:
+                over = s if renormalize else z[r][~np.isneginf(z[r])]
+                m = over.max()
+                s, total = np.exp(s - m), np.exp(over - m).sum()
+            else:
+                total = s.sum() if renormalize else 1.0
+            w[r, :len(chosen)] = (s if total == 0 else s / total) * scale
+    return ids, w

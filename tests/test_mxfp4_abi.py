@@ -63,6 +63,24 @@ def test_dequantize_refusals(q8, lib):
     assert call(rows=0) == q8.Q8_0_OK
 
 
+def test_topk_refusals(q8, lib):
+    def call(sel=FAKE, w=FAKE, logits=FAKE, bias=None, t=4, e=256, u=8, scoring=0):
+        return lib.moe_topk(sel, w, logits, bias, t, e, u, scoring, 1, 1.0, None)
+    assert call(e=0) == q8.Q8_0_EINVAL
+    assert call(e=1025) == q8.Q8_0_EINVAL
+    assert call(u=0) == q8.Q8_0_EINVAL
+    assert call(u=33) == q8.Q8_0_EINVAL
+    assert call(e=4, u=5) == q8.Q8_0_EINVAL
+    assert call(scoring=3) == q8.Q8_0_EINVAL
+    assert call(t=-1) == q8.Q8_0_EINVAL
+    assert call(t=1 << 29) == q8.Q8_0_EINVAL
+    for name in ("sel", "w", "logits"):
+        assert call(**{name: None}) == q8.Q8_0_EINVAL
+        assert call(**{name: FAKE + 2}) == q8.Q8_0_EALIGN
+    assert call(bias=FAKE + 1) == q8.Q8_0_EALIGN
+    assert call(t=0) == q8.Q8_0_OK
+
+
 def test_binding_refuses_host_tensors_and_wrong_shapes(q8):
     with pytest.raises(ValueError):
         q8.mxfp4_quantize(torch.zeros(2, 64))
@@ -78,3 +96,4 @@ def test_valid_calls_without_device_report_nodev(q8, lib):
         pytest.skip("a device is present")
     assert lib.mxfp4_quantize(FAKE, FAKE, FAKE, 0, 64, 2, 64, None) == q8.Q8_0_ENODEV
     assert lib.mxfp4_dequantize(FAKE, 0, FAKE, FAKE, 2, 64, None) == q8.Q8_0_ENODEV
+    assert lib.moe_topk(FAKE, FAKE, FAKE, None, 4, 256, 8, 0, 1, 1.0, None) == q8.Q8_0_ENODEV
