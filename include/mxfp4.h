@@ -59,6 +59,32 @@ int mxfp4_quantize(void *codes, void *scales, const void *x, int32_t x_type, int
 int mxfp4_dequantize(void *out, int32_t out_type, const void *codes, const void *scales,
                      int64_t n_rows, int64_t in_dim, hipStream_t stream);
 
+/* Workspace bytes of mxfp4_matmul's fastest plan for this shape (partial sums
+ * of a split over in_dim); 0 when it needs none or the shape is invalid. */
+size_t mxfp4_matmul_workspace_bytes(int64_t in_dim, int64_t out_dim, int64_t n_tok);
+
+/* MXFP4 product, the 4-bit counterpart of q8_0_matmul:
+ *   out[t][o] = sum_b 2^(sw[o][b] + sx[t][b] - 254) * sum_{i<32} w[o][b][i] * x[t][b][i]
+ *   out    : [n_tok][out_dim] of out_type, written (fp32 sums, rounded once).
+ *   w_*    : MXFP4 [out_dim][in_dim]; x_* : MXFP4 [n_tok][in_dim] (e.g. from
+ *            mxfp4_quantize).
+ *   workspace / workspace_bytes : optional scratch (16-byte aligned device
+ *            memory; its contents on entry do not matter).  With less than
+ *            mxfp4_matmul_workspace_bytes() the library picks a plan that fits;
+ *            NULL / 0 is always valid.  Calls that share a workspace must not
+ *            overlap in time.
+ * Products are exact and summed in fp32: |out - exact| <= (in_dim / 32 + 8) *
+ * 2^-23 * sum |w x| before the rounding to out_type.  A NaN block makes every
+ * output that uses it NaN.
+ * n_tok == 0 or out_dim == 0 is a successful no-op.
+ * Errors: in_dim % 32 != 0, in_dim == 0 or above 2^24 with work to do, out_dim
+ * or n_tok above 2^31 - 1, negative sizes, unknown type, null pointers ->
+ * Q8_0_EINVAL; codes or workspace not 16-byte aligned, out not aligned to its
+ * type -> Q8_0_EALIGN. */
+int mxfp4_matmul(void *out, int32_t out_type, const void *w_codes, const void *w_scales,
+                 int64_t in_dim, int64_t out_dim, const void *x_codes, const void *x_scales,
+                 int64_t n_tok, void *workspace, size_t workspace_bytes, hipStream_t stream);
+
 /* Scores of moe_topk, from a token's logits z. */
 enum {
     MOE_SOFTMAX = 0,      /* exp(z) / sum exp(z); ordered by z itself */
@@ -93,6 +119,60 @@ enum {
 int moe_topk(int32_t *selected, float *weights, const float *logits, const float *bias,
              int64_t n_tok, int32_t n_expert, int32_t n_used, int32_t scoring,
              int32_t renormalize, float scale, hipStream_t stream);
+
+#define MXFP4_MOE_MAX_TOKENS 64
+#define MXFP4_MOE_MAX_EXPERTS 512
+
+/* Arguments of mxfp4_moe_layer. */
+typedef struct mxfp4_moe_layer_args {
+    void *out;               /* [n_tok][d_model] of out_type, written                */
+    const void *x;           /* [n_tok][d_model] of x_type: the layer's input        */
+    int32_t out_type, x_type;
+    const float *logits;     /* fp32 [n_tok][n_expert]: router logits                */
+    const float *bias;       /* fp32 [n_expert], or NULL (as moe_topk)               */
+    int32_t n_expert;        /* 1 .. MXFP4_MOE_MAX_EXPERTS                           */
+    int32_t n_used;          /* experts per token, as moe_topk                       */
+    int32_t scoring;         /* MOE_SOFTMAX, ...                                     */
+    int32_t renormalize;
+    float scale;
+    float clamp;             /* SwiGLU limit; <= 0 or NaN: no clamp                  */
+    int64_t d_model;         /* expert input and output width, a multiple of 32      */
+    int64_t d_ff;            /* expert hidden width, a multiple of 32                */
+    int64_t n_tok;           /* 0 .. MXFP4_MOE_MAX_TOKENS                            */
+    const void *gate_codes, *gate_scales; /* MXFP4 [n_expert][d_ff][d_model]         */
+    const void *up_codes, *up_scales;     /* MXFP4 [n_expert][d_ff][d_model]         */
+    const void *down_codes, *down_scales; /* MXFP4 [n_expert][d_model][d_ff]         */
+    int32_t *selected;       /* optional int32 [n_tok][n_used]: moe_topk's ids       */
+    float *weights;          /* optional fp32 [n_tok][n_used]: moe_topk's weights    */
+} mxfp4_moe_layer_args;
+
+/* Workspace bytes mxfp4_moe_layer needs (routing tables and the quantized mid
+ * of every pair); 0 for sizes it refuses. */
+size_t mxfp4_moe_layer_workspace_bytes(int64_t n_tok, int32_t n_used, int32_t n_expert,
+                                       int64_t d_model, int64_t d_ff);
+
+/* The whole MoE layer for a few tokens, from router logits to the weighted sum
+ * of the experts, in two kernels (q8_0_moe_ffn is its 8-bit counterpart from
+ * given ids on).  For token t, with (e_j, w_j) = moe_topk of its logits:
+ *   x4    = mxfp4_quantize(x_t)
+ *   gate  = W_gate[e_j] x4, up = W_up[e_j] x4          (products as mxfp4_matmul)
+ *   mid   = silu(gate) * up, silu(g) = g / (1 + exp(-g)), after the optional
+ *           limits (gate from above, up to +-clamp)    (fp32)
+ *   out_t = sum_j w_j W_down[e_j] mxfp4_quantize(mid)  (fp32 sums, experts in a
+ *           fixed order, rounded once)
+ * Each touched expert's matrices are read once for all of its tokens.  Slots
+ * without an eligible expert add nothing: a token whose logits are all
+ * -infinity (padding) gives zeros.
+ *   workspace : device memory, 256-byte aligned, contents on entry do not
+ *     matter; calls that share one must not overlap in time.
+ * Errors: bad sizes (as above and moe_topk's; d_model and d_ff up to 2^20;
+ * n_expert * d_model * d_ff up to 2^46), unknown types or scoring, null
+ * pointers -> Q8_0_EINVAL; codes, x, out or workspace not 16-byte (workspace:
+ * 256-byte) aligned, other pointers not 4-byte aligned (scales: any) ->
+ * Q8_0_EALIGN; workspace smaller than mxfp4_moe_layer_workspace_bytes() ->
+ * Q8_0_EWORKSPACE. */
+int mxfp4_moe_layer(const mxfp4_moe_layer_args *args, void *workspace, size_t workspace_bytes,
+                    hipStream_t stream);
 
 #ifdef __cplusplus
 }

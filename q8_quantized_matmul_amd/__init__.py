@@ -377,5 +377,7 @@ def q8_0_debug_read_lds(seen: torch.Tensor, workgroups: int) -> None:
 
 # The MXFP4 operators and the MoE router (include/mxfp4.h).
 from .mxfp4 import (MOE_SIGMOID, MOE_SOFTMAX, MOE_SQRT_SOFTPLUS, MXFP4_BF16,  # noqa: E402
-                    MXFP4_BLOCK_ELEMS, MXFP4_F16, MXFP4_F32, Mxfp4, moe_topk, mxfp4_dequantize,
-                    mxfp4_quantize)
+                    MXFP4_BLOCK_ELEMS, MXFP4_F16, MXFP4_F32, MoeLayerArgs, Mxfp4, moe_topk,
+                    mxfp4_dequantize, mxfp4_matmul, mxfp4_matmul_workspace,
+                    mxfp4_matmul_workspace_bytes, mxfp4_moe_layer, mxfp4_moe_layer_workspace,
+                    mxfp4_moe_layer_workspace_bytes, mxfp4_quantize)

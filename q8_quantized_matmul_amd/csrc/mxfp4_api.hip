@@ -13,6 +13,9 @@ static_assert(MOE_SOFTMAX == mx::kSoftmax && MOE_SIGMOID == mx::kSigmoid &&
                   MOE_SQRT_SOFTPLUS == mx::kSqrtSoftplus &&
                   MOE_MAX_EXPERTS == mx::kMaxRouteExperts && MOE_MAX_USED == mx::kMaxUsed,
               "header and library agree on the router");
+static_assert(MXFP4_MOE_MAX_TOKENS == mx::kMaxLayerTokens &&
+                  MXFP4_MOE_MAX_EXPERTS == mx::kMaxLayerExperts,
+              "header and library agree on the layer");
 
 namespace {
 
@@ -32,6 +35,14 @@ int check_matrix(int64_t rows, int64_t k) {
   return Q8_0_OK;
 }
 
+// Sizes of a product: the kernels count blocks, rows and tokens in 32 bits.
+constexpr int64_t kMaxInDim = 1 << 24;
+int check_product(int64_t in_dim, int64_t out_dim, int64_t n_tok) {
+  if (in_dim < 0 || out_dim < 0 || n_tok < 0 || in_dim % MXFP4_BLOCK_ELEMS != 0) return Q8_0_EINVAL;
+  if (in_dim > kMaxInDim || out_dim > INT32_MAX || n_tok > INT32_MAX) return Q8_0_EINVAL;
+  return Q8_0_OK;
+}
+
 int check_route(const float *logits, const float *bias, int64_t n_tok, int32_t n_expert,
                 int32_t n_used, int32_t scoring) {
   if (n_tok < 0 || n_expert < 1 || n_expert > MOE_MAX_EXPERTS || n_used < 1 || n_used > n_expert ||
@@ -42,6 +53,44 @@ int check_route(const float *logits, const float *bias, int64_t n_tok, int32_t n
   if (!logits) return Q8_0_EINVAL;
   if (!aligned(logits, 4) || !aligned(bias, 4)) return Q8_0_EALIGN;
   return Q8_0_OK;
+}
+
+constexpr int64_t kMaxWidth = 1 << 20;
+constexpr int64_t kMaxExpertElems = int64_t{1} << 46;
+bool layer_sizes_ok(int64_t n_tok, int32_t n_used, int32_t n_expert, int64_t d_model, int64_t d_ff) {
+  return n_tok >= 0 && n_tok <= MXFP4_MOE_MAX_TOKENS && n_expert >= 1 &&
+         n_expert <= MXFP4_MOE_MAX_EXPERTS && n_used >= 1 && n_used <= n_expert &&
+         n_used <= MOE_MAX_USED && d_model > 0 && d_model <= kMaxWidth && d_ff > 0 &&
+         d_ff <= kMaxWidth && d_model % MXFP4_BLOCK_ELEMS == 0 && d_ff % MXFP4_BLOCK_ELEMS == 0 &&
+         d_model * d_ff <= kMaxExpertElems / n_expert;
+}
+
+int run_layer(const mxfp4_moe_layer_args *a, void *workspace, size_t workspace_bytes,
+              hipStream_t stream) {
+  if (!a || !layer_sizes_ok(a->n_tok, a->n_used, a->n_expert, a->d_model, a->d_ff) ||
+      !type_ok(a->out_type) || !type_ok(a->x_type))
+    return Q8_0_EINVAL;
+  int st = check_route(a->logits, a->bias, a->n_tok, a->n_expert, a->n_used, a->scoring);
+  if (st != Q8_0_OK || a->n_tok == 0) return st;
+  if (!a->out || !a->x) return Q8_0_EINVAL;
+  for (const void *p : {a->gate_codes, a->gate_scales, a->up_codes, a->up_scales, a->down_codes,
+                        a->down_scales})
+    if (!p) return Q8_0_EINVAL;
+  for (const void *p : {a->gate_codes, a->up_codes, a->down_codes, a->x, (const void *)a->out})
+    if (!aligned(p, 16)) return Q8_0_EALIGN;
+  if (!aligned(a->selected, 4) || !aligned(a->weights, 4)) return Q8_0_EALIGN;
+  if (!workspace || workspace_bytes < mx::moe_layer_workspace_bytes(a->n_tok, a->n_used, a->n_expert, a->d_ff))
+    return Q8_0_EWORKSPACE;
+  if (!aligned(workspace, 256)) return Q8_0_EALIGN;
+  if ((st = q8::check_device()) != Q8_0_OK) return st;
+  const mx::RouteArgs route{a->logits, a->bias, a->n_expert, a->n_used, a->scoring,
+                            a->renormalize != 0, a->scale};
+  auto u8 = [](const void *p) { return static_cast<const uint8_t *>(p); };
+  const mx::MoeLayer m{a->out, a->out_type, a->x, a->x_type, &route,
+                       u8(a->gate_codes), u8(a->gate_scales), u8(a->up_codes), u8(a->up_scales),
+                       u8(a->down_codes), u8(a->down_scales), a->d_model, a->d_ff, a->n_tok,
+                       a->clamp, a->selected, a->weights};
+  return status_of(mx::launch_moe_layer(m, static_cast<uint8_t *>(workspace), stream));
 }
 
 }  // namespace
@@ -73,6 +122,25 @@ int mxfp4_dequantize(void *out, int32_t out_type, const void *codes, const void 
                                          stream));
 }
 
+size_t mxfp4_matmul_workspace_bytes(int64_t, int64_t, int64_t) { return 0; }
+
+int mxfp4_matmul(void *out, int32_t out_type, const void *w_codes, const void *w_scales,
+                 int64_t in_dim, int64_t out_dim, const void *x_codes, const void *x_scales,
+                 int64_t n_tok, void *workspace, size_t workspace_bytes, hipStream_t stream) {
+  int st = check_product(in_dim, out_dim, n_tok);
+  if (st != Q8_0_OK || !type_ok(out_type)) return Q8_0_EINVAL;
+  if (n_tok == 0 || out_dim == 0) return Q8_0_OK;
+  if (in_dim == 0 || !out || !w_codes || !w_scales || !x_codes || !x_scales) return Q8_0_EINVAL;
+  if (!aligned(w_codes, 16) || !aligned(x_codes, 16) || !aligned(out, type_size(out_type)) ||
+      !aligned(workspace, 16))
+    return Q8_0_EALIGN;
+  if ((st = q8::check_device()) != Q8_0_OK) return st;
+  return status_of(mx::launch_matmul(
+      out, out_type, static_cast<const uint8_t *>(w_codes), static_cast<const uint8_t *>(w_scales),
+      in_dim, out_dim, static_cast<const uint8_t *>(x_codes),
+      static_cast<const uint8_t *>(x_scales), n_tok, stream));
+}
+
 int moe_topk(int32_t *selected, float *weights, const float *logits, const float *bias,
              int64_t n_tok, int32_t n_expert, int32_t n_used, int32_t scoring,
              int32_t renormalize, float scale, hipStream_t stream) {
@@ -83,6 +151,17 @@ int moe_topk(int32_t *selected, float *weights, const float *logits, const float
   if ((st = q8::check_device()) != Q8_0_OK) return st;
   const mx::RouteArgs a{logits, bias, n_expert, n_used, scoring, renormalize != 0, scale};
   return status_of(mx::launch_topk(a, n_tok, selected, weights, stream));
+}
+
+size_t mxfp4_moe_layer_workspace_bytes(int64_t n_tok, int32_t n_used, int32_t n_expert,
+                                       int64_t d_model, int64_t d_ff) {
+  if (!layer_sizes_ok(n_tok, n_used, n_expert, d_model, d_ff)) return 0;
+  return mx::moe_layer_workspace_bytes(n_tok, n_used, n_expert, d_ff);
+}
+
+int mxfp4_moe_layer(const mxfp4_moe_layer_args *args, void *workspace, size_t workspace_bytes,
+                    hipStream_t stream) {
+  return run_layer(args, workspace, workspace_bytes, stream);
 }
 
 }  // extern "C"

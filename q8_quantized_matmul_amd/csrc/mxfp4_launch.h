@@ -16,9 +16,32 @@ hipError_t launch_quantize(uint8_t *codes, uint8_t *scales, const void *x, int x
 hipError_t launch_dequantize(void *out, int out_type, const uint8_t *codes, const uint8_t *scales,
                              int64_t n_rows, int64_t in_dim, hipStream_t s);
 
+// mxfp4_matmul.hip
+hipError_t launch_matmul(void *out, int out_type, const uint8_t *w, const uint8_t *ws, int64_t in_dim,
+                         int64_t out_dim, const uint8_t *x, const uint8_t *xs, int64_t n_tok,
+                         hipStream_t s);
+
 // moe_topk.hip
 struct RouteArgs;
 hipError_t launch_topk(const RouteArgs &a, int64_t n_tok, int32_t *selected, float *weights,
                        hipStream_t s);
+
+// mxfp4_moe.hip: the whole MoE layer; buffers already validated.
+constexpr int kMaxLayerTokens = 64;
+constexpr int kMaxLayerExperts = 512;
+struct MoeLayer {
+  void *out;
+  int out_type;
+  const void *x;
+  int x_type;
+  const RouteArgs *route;
+  const uint8_t *gate, *gate_s, *up, *up_s, *down, *down_s;
+  int64_t d_model, d_ff, n_tok;
+  float clamp;
+  int32_t *selected;  // optional
+  float *weights;     // optional
+};
+size_t moe_layer_workspace_bytes(int64_t n_tok, int32_t n_used, int32_t n_expert, int64_t d_ff);
+hipError_t launch_moe_layer(const MoeLayer &m, uint8_t *ws, hipStream_t s);
 
 }  // namespace mx

@@ -1,0 +1,117 @@
+// mxfp4_matmul.hip -- the product of MXFP4 weights and MXFP4 rows,
+//   out[t][o] = sum_b 2^(sw[o][b] + sx[t][b] - 254) sum_i w[o][b][i] x[t][b][i].
+//
+// Streaming kernel.  With few tokens the product is bound by reading the
+// weights, 17 bytes per 32 values.  A wave takes 16 weight rows as the A operand
+// straight from memory to registers, steps of 512 values apart, and 16 tokens as
+// B (16x16x128 instructions: 16 of their 16 columns idle at one token, but the
+// matrix core still takes weights ten times faster than memory gives them).
+// ks waves of a workgroup split a row's steps and are joined in LDS in wave
+// order, so that short rows and few rows still give the memory enough waves.
+#include "mxfp4_mfma.h"
+
+namespace mx {
+namespace {
+
+constexpr int kWaves = 8;
+
+struct MatmulArgs {
+  void *out;
+  const uint8_t *w, *ws, *x, *xs;
+  int32_t nb;        // blocks of a row
+  int64_t n, t;      // weight rows, tokens
+  int32_t ks;        // waves along K: a power of two <= kWaves
+  bool wide;         // rows of out are aligned for stores of four values
+};
+
+// NT: tiles of 16 tokens a workgroup takes.
+template <int NT, bool WHOLE, int TYPE>
+__global__ __launch_bounds__(64 * kWaves) void stream_kernel(const MatmulArgs a) {
+  __shared__ f32x4 part[kWaves * NT * 64];
+  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+  const int kq = wave & (a.ks - 1), rt = wave / a.ks;
+  const int tiles = kWaves / a.ks;  // row tiles of the workgroup
+  const int row = lane & 15, g = lane >> 4;
+  const int64_t o0 = ((int64_t)blockIdx.x * tiles + rt) * 16;
+  const int64_t t0 = (int64_t)blockIdx.y * (16 * NT);
+  // Rows past the ends are read as the last row; what they give is not stored.
+  const int64_t wr = min(o0 + row, a.n - 1);
+  const uint8_t *wc = a.w + wr * (a.nb * 16), *wsc = a.ws + wr * a.nb;
+  const uint8_t *xc[NT], *xsc[NT];
+#pragma unroll
+  for (int j = 0; j < NT; ++j) {
+    const int64_t xr = min(t0 + 16 * j + row, a.t - 1);
+    xc[j] = a.x + xr * (a.nb * 16);
+    xsc[j] = a.xs + xr * a.nb;
+  }
+  f32x4 acc[NT];
+#pragma unroll
+  for (int j = 0; j < NT; ++j) acc[j] = f32x4{0, 0, 0, 0};
+
+  const int steps = (a.nb + kStepBlocks - 1) / kStepBlocks;
+  if (o0 < a.n) {
+    for (int s = kq; s < steps; s += a.ks) {
+      const int b0 = s * kStepBlocks + 4 * g;
+      Blocks4 A, B[NT];
+      load_blocks<WHOLE>(wc, wsc, b0, a.nb, A);
+#pragma unroll
+      for (int j = 0; j < NT; ++j) load_blocks<WHOLE>(xc[j], xsc[j], b0, a.nb, B[j]);
+#pragma unroll
+      for (int j = 0; j < NT; ++j) acc[j] = mfma_blocks4(A, B[j], acc[j]);
+    }
+  }
+  if (a.ks > 1) {
+#pragma unroll
+    for (int j = 0; j < NT; ++j) part[(wave * NT + j) * 64 + lane] = acc[j];
+    __syncthreads();
+  }
+  // Wave kq of a row tile's ks waves joins and stores token tiles kq, kq + ks, ...
+#pragma unroll
+  for (int j = 0; j < NT; ++j) {
+    if ((j & (a.ks - 1)) != kq) continue;
+    f32x4 v = acc[j];
+    if (a.ks > 1) {
+      v = part[((wave - kq) * NT + j) * 64 + lane];
+      for (int q = 1; q < a.ks; ++q) v += part[((wave - kq + q) * NT + j) * 64 + lane];
+    }
+    const int64_t t = t0 + 16 * j + row, o = o0 + 4 * g;
+    if (t < a.t && o < a.n) store4<TYPE>(a.out, t * a.n + o, v, (int)min<int64_t>(4, a.n - o), a.wide);
+  }
+}
+
+bool a4(const void *p) { return (reinterpret_cast<uintptr_t>(p) & 3) == 0; }
+
+}  // namespace
+
+hipError_t launch_matmul(void *out, int out_type, const uint8_t *w, const uint8_t *ws, int64_t in_dim,
+                         int64_t out_dim, const uint8_t *x, const uint8_t *xs, int64_t n_tok,
+                         hipStream_t s) {
+  const int nb = (int)(in_dim / kBlock);
+  const int size = out_type == kF32 ? 4 : 2;
+  MatmulArgs a{out, w, ws, x, xs, nb, out_dim, n_tok, 1, false};
+  a.wide = out_dim % 4 == 0 && (reinterpret_cast<uintptr_t>(out) & (4 * size - 1)) == 0;
+  const bool whole = nb % 4 == 0 && a4(ws) && a4(xs);
+  const int64_t tiles = (out_dim + 15) / 16, steps = (nb + kStepBlocks - 1) / kStepBlocks;
+  const int nt = n_tok <= 16 ? 1 : n_tok <= 32 ? 2 : 4;
+  while (a.ks < kWaves && a.ks < steps && tiles * a.ks < 4096) a.ks *= 2;
+  const int64_t per_wg = kWaves / a.ks;
+  const dim3 grid((uint32_t)((tiles + per_wg - 1) / per_wg), (uint32_t)((n_tok + 16 * nt - 1) / (16 * nt)));
+  auto go = [&](auto kernel) { hipLaunchKernelGGL(kernel, grid, dim3(64 * kWaves), 0, s, a); };
+  auto by_type = [&](auto nt_c, auto whole_c) {
+    constexpr int NT = decltype(nt_c)::value;
+    constexpr bool W = decltype(whole_c)::value;
+    if (out_type == kF32) go(stream_kernel<NT, W, kF32>);
+    else if (out_type == kBF16) go(stream_kernel<NT, W, kBF16>);
+    else go(stream_kernel<NT, W, kF16>);
+  };
+  auto by_nt = [&](auto whole_c) {
+    if (nt == 1) by_type(std::integral_constant<int, 1>{}, whole_c);
+    else if (nt == 2) by_type(std::integral_constant<int, 2>{}, whole_c);
+    else by_type(std::integral_constant<int, 4>{}, whole_c);
+  };
+  if (whole) by_nt(std::true_type{});
+  else by_nt(std::false_type{});
+  return hipGetLastError();
+}
+
+}  // namespace mx

@@ -20,11 +20,26 @@ MXFP4_F32, MXFP4_BF16, MXFP4_F16 = 0, 1, 2
 MOE_SOFTMAX, MOE_SIGMOID, MOE_SQRT_SOFTPLUS = 0, 1, 2
 _TYPES = {torch.float32: MXFP4_F32, torch.bfloat16: MXFP4_BF16, torch.float16: MXFP4_F16}
 
+class MoeLayerArgs(ctypes.Structure):
+    """struct mxfp4_moe_layer_args."""
+    _fields_ = [("out", _vp), ("x", _vp), ("out_type", _i32), ("x_type", _i32), ("logits", _vp),
+                ("bias", _vp), ("n_expert", _i32), ("n_used", _i32), ("scoring", _i32),
+                ("renormalize", _i32), ("scale", ctypes.c_float), ("clamp", ctypes.c_float),
+                ("d_model", _i64), ("d_ff", _i64), ("n_tok", _i64), ("gate_codes", _vp),
+                ("gate_scales", _vp), ("up_codes", _vp), ("up_scales", _vp), ("down_codes", _vp),
+                ("down_scales", _vp), ("selected", _vp), ("weights", _vp)]
+
+
 _sig = {
     "mxfp4_quantize": ([_vp, _vp, _vp, _i32, _i64, _i64, _i64, _vp], ctypes.c_int),
     "mxfp4_dequantize": ([_vp, _i32, _vp, _vp, _i64, _i64, _vp], ctypes.c_int),
+    "mxfp4_matmul_workspace_bytes": ([_i64, _i64, _i64], _sz),
+    "mxfp4_matmul": ([_vp, _i32, _vp, _vp, _i64, _i64, _vp, _vp, _i64, _vp, _sz, _vp],
+                     ctypes.c_int),
     "moe_topk": ([_vp, _vp, _vp, _vp, _i64, _i32, _i32, _i32, _i32, ctypes.c_float, _vp],
                  ctypes.c_int),
+    "mxfp4_moe_layer_workspace_bytes": ([_i64, _i32, _i32, _i64, _i64], _sz),
+    "mxfp4_moe_layer": ([ctypes.POINTER(MoeLayerArgs), _vp, _sz, _vp], ctypes.c_int),
 }
 for _name, (_args, _res) in _sig.items():
     _fn = getattr(_lib, _name)
@@ -131,6 +146,48 @@ def mxfp4_dequantize(m: Mxfp4, dtype: torch.dtype = torch.float32,
     return out
 
 
+def mxfp4_matmul_workspace_bytes(in_dim: int, out_dim: int, n_tok: int) -> int:
+    return int(_lib.mxfp4_matmul_workspace_bytes(in_dim, out_dim, n_tok))
+
+
+def mxfp4_matmul_workspace(in_dim: int, out_dim: int, n_tok: int, device="cuda") -> torch.Tensor:
+    """Scratch for mxfp4_matmul calls of this shape (contents do not matter)."""
+    return torch.empty(mxfp4_matmul_workspace_bytes(in_dim, out_dim, n_tok), dtype=torch.uint8,
+                       device=device)
+
+
+def _scratch(t, need: int, device):
+    """(pointer, bytes) of the caller's scratch, or of `need` bytes allocated now; the
+    allocator keeps a freed tensor's memory for later work on the same stream."""
+    if t is None:
+        if need == 0:
+            return None, 0, None
+        t = torch.empty(need, dtype=torch.uint8, device=device)
+    return _ptr(t, "workspace", torch.uint8, device), t.numel(), t
+
+
+def mxfp4_matmul(w: Mxfp4, x: Mxfp4, out: torch.Tensor = None,
+                 out_dtype: torch.dtype = torch.float32,
+                 workspace: torch.Tensor = None) -> torch.Tensor:
+    """out [n_tok][out_dim] = x [n_tok][k] times w [out_dim][k] transposed, both MXFP4,
+    as float32 (or out_dtype, or out's type).  Without a workspace one is
+    allocated for shapes that can use it."""
+    device = _device(x[0], "x.codes")
+    wc, wsc, w_lead, k = _matrix(w, "w", device)
+    xc, xsc, x_lead, xk = _matrix(x, "x", device)
+    if len(w_lead) != 1 or len(x_lead) != 1 or xk != k:
+        raise ValueError("w must be [out_dim][k] and x [n_tok][k]")
+    out_dim, n_tok = w_lead[0], x_lead[0]
+    if out is None:
+        out = torch.empty((n_tok, out_dim), dtype=out_dtype, device=device)
+    _shape(out, "out", n_tok, out_dim)
+    ws, ws_bytes, keep = _scratch(workspace, mxfp4_matmul_workspace_bytes(k, out_dim, n_tok)
+                                  if workspace is None else 0, device)
+    _run("mxfp4_matmul", device, _ptr(out, "out", out.dtype, device), _type(out.dtype, "out"), wc,
+         wsc, k, out_dim, xc, xsc, n_tok, ws, ws_bytes)
+    return out
+
+
 def moe_topk(logits: torch.Tensor, n_used: int, bias: torch.Tensor = None,
              scoring: int = MOE_SOFTMAX, renormalize: bool = True, scale: float = 1.0,
              selected: torch.Tensor = None, weights: torch.Tensor = None):
@@ -155,3 +212,64 @@ def moe_topk(logits: torch.Tensor, n_used: int, bias: torch.Tensor = None,
          _ptr(logits, "logits", torch.float32, device), bias, n_tok, n_expert, n_used, scoring,
          int(renormalize), scale)
     return selected, weights
+
+
+def mxfp4_moe_layer_workspace_bytes(n_tok: int, n_used: int, n_expert: int, d_model: int,
+                                    d_ff: int) -> int:
+    return int(_lib.mxfp4_moe_layer_workspace_bytes(n_tok, n_used, n_expert, d_model, d_ff))
+
+
+def mxfp4_moe_layer_workspace(n_tok: int, n_used: int, n_expert: int, d_model: int, d_ff: int,
+                              device="cuda") -> torch.Tensor:
+    """Scratch for mxfp4_moe_layer calls of these sizes (contents do not matter)."""
+    n = mxfp4_moe_layer_workspace_bytes(n_tok, n_used, n_expert, d_model, d_ff)
+    return torch.empty(n, dtype=torch.uint8, device=device)
+
+
+def mxfp4_moe_layer(x: torch.Tensor, logits: torch.Tensor, gate: Mxfp4, up: Mxfp4, down: Mxfp4,
+                    n_used: int, bias: torch.Tensor = None, scoring: int = MOE_SOFTMAX,
+                    renormalize: bool = True, scale: float = 1.0, clamp: float = 0.0,
+                    out: torch.Tensor = None, out_dtype: torch.dtype = None,
+                    selected: torch.Tensor = None, weights: torch.Tensor = None,
+                    workspace: torch.Tensor = None):
+    """The whole MoE layer for up to 64 tokens: x (float32, bfloat16 or float16
+    [n_tok][d_model]) and router logits (float32 [n_tok][n_expert]) through the
+    chosen experts' MXFP4 matrices gate, up [n_expert][d_ff][d_model] and down
+    [n_expert][d_model][d_ff].  Returns (out [n_tok][d_model] of out_dtype, by
+    default x's, selected, weights), the last two as moe_topk gives them."""
+    device = _device(x, "x")
+    if x.dim() != 2 or logits.dim() != 2:
+        raise ValueError("x must be [n_tok][d_model] and logits [n_tok][n_expert]")
+    n_tok, d_model = x.shape
+    n_expert = logits.shape[1]
+    gc, gs, g_lead, gk = _matrix(gate, "gate", device)
+    uc, us, u_lead, uk = _matrix(up, "up", device)
+    dc, ds, d_lead, d_ff = _matrix(down, "down", device)
+    if (tuple(g_lead) != (n_expert, d_ff) or tuple(u_lead) != (n_expert, d_ff)
+            or tuple(d_lead) != (n_expert, d_model) or gk != d_model or uk != d_model
+            or logits.shape[0] != n_tok):
+        raise ValueError("x [n_tok][d_model], logits [n_tok][n_expert], gate and up [n_expert][d_ff]"
+                         "[d_model] and down [n_expert][d_model][d_ff] do not fit together")
+    if bias is not None:
+        _shape(bias, "bias", n_expert)
+        bias = _ptr(bias, "bias", torch.float32, device)
+    if out is None:
+        out = torch.empty((n_tok, d_model), dtype=out_dtype or x.dtype, device=device)
+    if selected is None:
+        selected = torch.empty((n_tok, n_used), dtype=torch.int32, device=device)
+    if weights is None:
+        weights = torch.empty((n_tok, n_used), dtype=torch.float32, device=device)
+    _shape(out, "out", n_tok, d_model)
+    _shape(selected, "selected", n_tok, n_used)
+    _shape(weights, "weights", n_tok, n_used)
+    ws, ws_bytes, keep = _scratch(
+        workspace, mxfp4_moe_layer_workspace_bytes(n_tok, n_used, n_expert, d_model, d_ff)
+        if workspace is None else 0, device)
+    args = MoeLayerArgs(_ptr(out, "out", out.dtype, device), _ptr(x, "x", x.dtype, device),
+                        _type(out.dtype, "out"), _type(x.dtype, "x"),
+                        _ptr(logits, "logits", torch.float32, device), bias, n_expert, n_used,
+                        scoring, int(renormalize), scale, clamp, d_model, d_ff, n_tok, gc, gs, uc,
+                        us, dc, ds, _ptr(selected, "selected", torch.int32, device),
+                        _ptr(weights, "weights", torch.float32, device))
+    _run("mxfp4_moe_layer", device, ctypes.byref(args), ws, ws_bytes)
+    return out, selected, weights

@@ -86,3 +86,69 @@ def route(logits, n_used, bias=None, scoring=0, renormalize=True, scale=1.0):
                 total = s.sum() if renormalize else 1.0
             w[r, :len(chosen)] = (s if total == 0 else s / total) * scale
     return ids, w
+
+
+def _rounded(v, e):
+    """v rounded to the e2m1 grid at scale 2^e (float64, elementwise)."""
+    a = np.minimum(np.abs(v) / np.exp2(e), 6.0)
+    step = np.where(a < 2, 0.5, np.where(a < 4, 1.0, 2.0))
+    return np.copysign(np.rint(a / step) * step, v) * np.exp2(e)
+
+
+def _requantized(mid, delta):
+    """The quantized values of mid [n][k], and how far those of any numbers
+    within delta of it may be from them (next to a rounding boundary, or in a
+    block whose maximum may lie on either side of a power of two)."""
+    b, d = mid.reshape(len(mid), -1, 32), delta.reshape(len(mid), -1, 32)
+
+    def exponent(m):
+        _, e = np.frexp(m)
+        return np.where(m > 0, np.maximum(e - 3, -127), -127).astype(np.float64)[..., None]
+    q = _rounded(b, exponent(np.abs(b).max(-1)))
+    low = exponent(np.maximum(np.abs(b) - d, 0.0).max(-1))
+    high = exponent((np.abs(b) + d).max(-1))
+    off = np.zeros_like(b)
+    for e in (low, high):
+        for end in (b - d, b + d):
+            off = np.maximum(off, np.abs(_rounded(end, e) - q))
+    return q.reshape(mid.shape), off.reshape(mid.shape)
+
+
+def moe_layer(x, logits, gate, up, down, n_used, bias=None, scoring=0, renormalize=True, scale=1.0,
+              clamp=0.0, half=0.0):
+    """(out, tolerance, ids, weights) of the whole layer in 64 bits, from float64
+    x and (codes, scales) matrices [e][n][k].
+
+    The tolerance follows the fp32 roundings through the formula: a product's
+    (k / 32 + 8) steps of sum |w x|, carried through silu (|silu'| < 1.1) with
+    16 half steps for its own evaluation; mid values that may fall on the other
+    side of a rounding boundary; the down product's steps; the weights' roundings
+    and one per expert in the sum; `half` for the rounding of the output."""
+    step = 2.0 ** -23
+    x4 = values(*quantize(x))
+    t, d = x4.shape
+    f = gate[0].shape[1]
+    ids, weights = route(logits, n_used, bias, scoring, renormalize, scale)
+    z = np.asarray(logits, np.float64)
+    z = z[np.isfinite(z) & (z > -1e30)]
+    wrel = ((float(z.max() - z.min()) if z.size else 0.0) + 32) * step / 2
+    out, tol, mag = np.zeros((t, d)), np.zeros((t, d)), np.zeros((t, d))
+    for e in np.unique(ids[ids >= 0]):
+        tok, slot = np.nonzero(ids == e)
+        wg, wu, wd = (values(m[0][e], m[1][e]) for m in (gate, up, down))
+        g, u = x4[tok] @ wg.T, x4[tok] @ wu.T
+        dg, du = ((d / 32 + 8) * step * (np.abs(x4[tok]) @ np.abs(w).T) for w in (wg, wu))
+        if clamp > 0:
+            g, u = np.minimum(g, clamp), np.clip(u, -clamp, clamp)
+        silu = g / (1 + np.exp(-g))
+        mid = silu * u
+        delta = 1.1 * np.abs(u) * dg + np.abs(silu) * du + 1.1 * dg * du + 8 * step * np.abs(mid)
+        q, off = _requantized(mid, delta)
+        y = q @ wd.T
+        dy = off @ np.abs(wd).T + (f / 32 + 8) * step * ((np.abs(q) + off) @ np.abs(wd).T)
+        w = weights[tok, slot][:, None]
+        np.add.at(out, tok, w * y)
+        np.add.at(tol, tok, np.abs(w) * dy * (1 + wrel))
+        np.add.at(mag, tok, np.abs(w * y))
+    tol += mag * (wrel + (n_used + 2) * step / 2) + half * np.abs(out) + 1e-30
+    return out, tol, ids, weights

@@ -63,6 +63,26 @@ def test_dequantize_refusals(q8, lib):
     assert call(rows=0) == q8.Q8_0_OK
 
 
+def test_matmul_refusals(q8, lib):
+    def call(out=FAKE, out_type=0, wc=FAKE, ws=FAKE, k=64, n=16, xc=FAKE, xs=FAKE, t=2, work=None, nbytes=0):
+        return lib.mxfp4_matmul(out, out_type, wc, ws, k, n, xc, xs, t, work, nbytes, None)
+    assert call(k=48) == q8.Q8_0_EINVAL
+    assert call(k=0) == q8.Q8_0_EINVAL
+    assert call(k=(1 << 24) + 32) == q8.Q8_0_EINVAL
+    assert call(n=-1) == q8.Q8_0_EINVAL
+    assert call(t=1 << 31) == q8.Q8_0_EINVAL
+    assert call(out_type=7) == q8.Q8_0_EINVAL
+    for name in ("out", "wc", "ws", "xc", "xs"):
+        assert call(**{name: None}) == q8.Q8_0_EINVAL
+    assert call(wc=FAKE + 8) == q8.Q8_0_EALIGN
+    assert call(xc=FAKE + 4) == q8.Q8_0_EALIGN
+    assert call(out=FAKE + 2) == q8.Q8_0_EALIGN
+    assert call(out=FAKE + 1, out_type=1) == q8.Q8_0_EALIGN
+    assert call(work=FAKE + 8, nbytes=64) == q8.Q8_0_EALIGN
+    assert call(t=0) == q8.Q8_0_OK
+    assert call(n=0) == q8.Q8_0_OK
+
+
 def test_topk_refusals(q8, lib):
     def call(sel=FAKE, w=FAKE, logits=FAKE, bias=None, t=4, e=256, u=8, scoring=0):
         return lib.moe_topk(sel, w, logits, bias, t, e, u, scoring, 1, 1.0, None)
@@ -81,6 +101,38 @@ def test_topk_refusals(q8, lib):
     assert call(t=0) == q8.Q8_0_OK
 
 
+def test_layer_refusals(q8, lib):
+    need = q8.mxfp4_moe_layer_workspace_bytes(8, 4, 16, 256, 128)
+    assert need >= 8 * 4 * (64 + 4)
+
+    def call(ws=FAKE, ws_bytes=need, **kw):
+        f = dict(out=FAKE, x=FAKE, out_type=1, x_type=1, logits=FAKE, bias=None, n_expert=16, n_used=4,
+                 scoring=0, renormalize=1, scale=1.0, clamp=0.0, d_model=256, d_ff=128, n_tok=8,
+                 gate_codes=FAKE, gate_scales=FAKE, up_codes=FAKE, up_scales=FAKE, down_codes=FAKE,
+                 down_scales=FAKE, selected=None, weights=None)
+        f.update(kw)
+        return lib.mxfp4_moe_layer(ctypes.byref(q8.MoeLayerArgs(**f)), ws, ws_bytes, None)
+
+    assert lib.mxfp4_moe_layer(None, FAKE, need, None) == q8.Q8_0_EINVAL
+    for bad in (dict(n_tok=65), dict(n_tok=-1), dict(n_expert=0), dict(n_expert=513), dict(n_used=0),
+                dict(n_used=17), dict(d_model=100), dict(d_model=0), dict(d_ff=48), dict(d_ff=1 << 21),
+                dict(scoring=3), dict(x_type=3), dict(out_type=-1), dict(n_expert=512, d_model=1 << 20, d_ff=1 << 20)):
+        assert call(**bad) == q8.Q8_0_EINVAL, bad
+    for name in ("out", "x", "logits", "gate_codes", "gate_scales", "up_codes", "up_scales", "down_codes", "down_scales"):
+        assert call(**{name: None}) == q8.Q8_0_EINVAL, name
+    for name in ("out", "x", "gate_codes", "up_codes", "down_codes"):
+        assert call(**{name: FAKE + 8}) == q8.Q8_0_EALIGN, name
+    for name in ("logits", "bias", "selected", "weights"):
+        assert call(**{name: FAKE + 2}) == q8.Q8_0_EALIGN, name
+    assert call(ws=None) == q8.Q8_0_EWORKSPACE
+    assert call(ws_bytes=need - 1) == q8.Q8_0_EWORKSPACE
+    assert call(ws=FAKE + 64) == q8.Q8_0_EALIGN
+    assert call(n_tok=0) == q8.Q8_0_OK
+    assert q8.mxfp4_moe_layer_workspace_bytes(65, 4, 16, 256, 128) == 0
+    if torch.cuda.device_count() == 0:
+        assert call() == q8.Q8_0_ENODEV
+
+
 def test_binding_refuses_host_tensors_and_wrong_shapes(q8):
     with pytest.raises(ValueError):
         q8.mxfp4_quantize(torch.zeros(2, 64))
@@ -97,3 +149,4 @@ def test_valid_calls_without_device_report_nodev(q8, lib):
     assert lib.mxfp4_quantize(FAKE, FAKE, FAKE, 0, 64, 2, 64, None) == q8.Q8_0_ENODEV
     assert lib.mxfp4_dequantize(FAKE, 0, FAKE, FAKE, 2, 64, None) == q8.Q8_0_ENODEV
     assert lib.moe_topk(FAKE, FAKE, FAKE, None, 4, 256, 8, 0, 1, 1.0, None) == q8.Q8_0_ENODEV
+    assert lib.mxfp4_matmul(FAKE, 0, FAKE, FAKE, 64, 16, FAKE, FAKE, 2, None, 0, None) == q8.Q8_0_ENODEV
