@@ -14,7 +14,7 @@ CSRC = os.path.join(PKG, "csrc")
 LIB = os.path.join(PKG, "libq8_0.so")
 SOURCES = ["api.hip", "quantize.hip", "matvec.hip", "moe.hip", "gemm.hip", "skinny.hip", "probe.hip",
            "debug.hip", "mxfp4_api.hip", "mxfp4_quantize.hip",
-           "mxfp4_matmul.hip", "mxfp4_moe.hip", "moe_topk.hip"]
+           "mxfp4_matmul.hip", "mxfp4_gemm.hip", "mxfp4_moe.hip", "moe_topk.hip"]
 
 # -packed-fp32-ops: keep the compiler from emitting packed fp32 VALU forms.
 # No fast-math: the quantizer relies on IEEE division and roundf.

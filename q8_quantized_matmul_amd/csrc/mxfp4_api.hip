@@ -43,6 +43,8 @@ int check_product(int64_t in_dim, int64_t out_dim, int64_t n_tok) {
   return Q8_0_OK;
 }
 
+bool use_gemm(int64_t in_dim, int64_t n_tok) { return n_tok > 64 && in_dim >= 128; }
+
 int check_route(const float *logits, const float *bias, int64_t n_tok, int32_t n_expert,
                 int32_t n_used, int32_t scoring) {
   if (n_tok < 0 || n_expert < 1 || n_expert > MOE_MAX_EXPERTS || n_used < 1 || n_used > n_expert ||
@@ -122,7 +124,11 @@ int mxfp4_dequantize(void *out, int32_t out_type, const void *codes, const void 
                                          stream));
 }
 
-size_t mxfp4_matmul_workspace_bytes(int64_t, int64_t, int64_t) { return 0; }
+size_t mxfp4_matmul_workspace_bytes(int64_t in_dim, int64_t out_dim, int64_t n_tok) {
+  if (check_product(in_dim, out_dim, n_tok) != Q8_0_OK || in_dim == 0 || out_dim == 0 || n_tok == 0)
+    return 0;
+  return use_gemm(in_dim, n_tok) ? mx::gemm_workspace_bytes(in_dim, out_dim, n_tok) : 0;
+}
 
 int mxfp4_matmul(void *out, int32_t out_type, const void *w_codes, const void *w_scales,
                  int64_t in_dim, int64_t out_dim, const void *x_codes, const void *x_scales,
@@ -135,10 +141,14 @@ int mxfp4_matmul(void *out, int32_t out_type, const void *w_codes, const void *w
       !aligned(workspace, 16))
     return Q8_0_EALIGN;
   if ((st = q8::check_device()) != Q8_0_OK) return st;
-  return status_of(mx::launch_matmul(
-      out, out_type, static_cast<const uint8_t *>(w_codes), static_cast<const uint8_t *>(w_scales),
-      in_dim, out_dim, static_cast<const uint8_t *>(x_codes),
-      static_cast<const uint8_t *>(x_scales), n_tok, stream));
+  const auto *w = static_cast<const uint8_t *>(w_codes), *ws = static_cast<const uint8_t *>(w_scales);
+  const auto *x = static_cast<const uint8_t *>(x_codes), *xs = static_cast<const uint8_t *>(x_scales);
+  if (use_gemm(in_dim, n_tok)) {
+    const mx::GemmPlan p = mx::gemm_plan(in_dim, out_dim, n_tok, workspace ? workspace_bytes : 0);
+    return status_of(mx::launch_gemm(p, out, out_type, w, ws, in_dim, out_dim, x, xs, n_tok,
+                                     workspace, stream));
+  }
+  return status_of(mx::launch_matmul(out, out_type, w, ws, in_dim, out_dim, x, xs, n_tok, stream));
 }
 
 int moe_topk(int32_t *selected, float *weights, const float *logits, const float *bias,

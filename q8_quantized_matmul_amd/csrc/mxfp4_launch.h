@@ -21,6 +21,16 @@ hipError_t launch_matmul(void *out, int out_type, const uint8_t *w, const uint8_
                          int64_t out_dim, const uint8_t *x, const uint8_t *xs, int64_t n_tok,
                          hipStream_t s);
 
+// mxfp4_gemm.hip: for many tokens.  in_dim >= 128 (a row's scales are read four at a time).
+struct GemmPlan {
+  int tile, splits, stages_per_split;
+};
+GemmPlan gemm_plan(int64_t in_dim, int64_t out_dim, int64_t n_tok, size_t ws_bytes);
+size_t gemm_workspace_bytes(int64_t in_dim, int64_t out_dim, int64_t n_tok);
+hipError_t launch_gemm(const GemmPlan &p, void *out, int out_type, const uint8_t *w, const uint8_t *ws,
+                       int64_t in_dim, int64_t out_dim, const uint8_t *x, const uint8_t *xs,
+                       int64_t n_tok, void *workspace, hipStream_t s);
+
 // moe_topk.hip
 struct RouteArgs;
 hipError_t launch_topk(const RouteArgs &a, int64_t n_tok, int32_t *selected, float *weights,
