@@ -43,7 +43,7 @@ int check_product(int64_t in_dim, int64_t out_dim, int64_t n_tok) {
   return Q8_0_OK;
 }
 
-bool use_gemm(int64_t in_dim, int64_t n_tok) { return n_tok > 64 && in_dim >= 128; }
+bool use_gemm(int64_t in_dim, int64_t n_tok) { return n_tok > 64 && in_dim >= 256; }
 
 int check_route(const float *logits, const float *bias, int64_t n_tok, int32_t n_expert,
                 int32_t n_used, int32_t scoring) {

@@ -10,9 +10,13 @@
 // LDS: 128 bytes a row; the 16-byte block c of row r lies at position c ^ (r % 8),
 // which the copies get by reading that block from memory (a lane's place in LDS
 // is fixed, its address in memory is not) and which makes the eight rows that are
-// read together use all banks once.  A lane's block of instruction s (of a
-// stage's four) is block 4 h + s, h its half, so the four scale bytes it needs
-// are one dword: loaded straight to registers, a stage ahead.
+// read together use all banks once.
+//
+// A lane's block of instruction s (of a stage's four) is block 4 h + s, h its half,
+// so the four scale bytes it needs are one dword, the scale operand.  They go
+// straight to registers: scattered loads, a row each, that cost as many cache
+// lookups whatever they fetch, so a lane fetches eight bytes for two stages and
+// trades one dword with the lane of the other half.
 //
 // Blocks past the end of a row are read from inside the row and given the scale
 // byte 0 on both sides, whose products (below 2^-240) vanish in fp32; rows past
@@ -41,16 +45,23 @@ __device__ __forceinline__ void copy_to_lds(const uint8_t *src, uint8_t *dst) {
   __builtin_amdgcn_global_load_lds(src, dst, 16, 0, 0);
 }
 
-// Four scale bytes at any address.  A lane reads those of blocks b..b+3, or, near
-// the end of a row of nb >= 4 blocks, of the row's last four, and shifts them down
-// to b when it uses them (zero past the end).
-__device__ __forceinline__ uint32_t load_scales(const uint8_t *p) {
-  typedef uint32_t u32_a1 __attribute__((aligned(1)));
-  return *reinterpret_cast<const u32_a1 *>(p);
+// Eight scale bytes at any address.  A lane reads those of blocks b..b+7, or, near
+// the end of a row of nb >= 8 blocks, of the row's last eight, and shifts them
+// down to b when it uses them (zero past the end).
+__device__ __forceinline__ uint64_t load_scales(const uint8_t *p) {
+  typedef uint64_t u64_a1 __attribute__((aligned(1)));
+  return *reinterpret_cast<const u64_a1 *>(p);
 }
-__device__ __forceinline__ uint32_t shift_scales(uint32_t v, int b, int nb) {
-  const int half = 4 * min(max(b + 4 - nb, 0), 4);  // bits; in two steps, so that 32 gives zero
+__device__ __forceinline__ uint64_t shift_scales(uint64_t v, int b, int nb) {
+  const int half = 4 * min(max(b + 8 - nb, 0), 8);  // bits; in two steps, so that 64 gives zero
   return (v >> half) >> half;
+}
+// Half h of the wave holds the scales of blocks 8 h + 0..7 of its row's sixteen;
+// it needs blocks 4 h + 0..3 of the first eight (first) and of the last eight.
+__device__ __forceinline__ void split_scales(uint64_t v, uint32_t &first, uint32_t &second) {
+  const auto r = __builtin_amdgcn_permlane32_swap((uint32_t)v, (uint32_t)(v >> 32), false, false);
+  first = r[0];
+  second = r[1];
 }
 
 // Workgroups of one XCD (consecutive ids go round the eight) take neighbouring
@@ -124,20 +135,21 @@ __global__ __launch_bounds__(64 * WM * WN, 1) void gemm_kernel(const GemmArgs a)
 #pragma unroll
   for (int j = 0; j < TN; ++j)
     sx[j] = (uint32_t)(min(t0 + 32 * (wn * TN + j) + lrow, a.t - 1) - t0) * (uint32_t)a.nb;
-  uint32_t dw[TM], dx[TN], ndw[TM], ndx[TN];  // this stage's scales, the next one's
+  uint64_t nw[TM], nx[TN];              // scales of the next two stages
+  uint32_t dw[2][TM], dx[2][TN];        // of these two
   auto load_next_scales = [&](int st) {
-    const uint32_t b = (uint32_t)min(st * kStageBlocks + 4 * h, a.nb - 4);
+    const uint32_t b = (uint32_t)min(st * kStageBlocks + 8 * h, a.nb - 8);
 #pragma unroll
-    for (int i = 0; i < TM; ++i) ndw[i] = load_scales(wsbase + (sw[i] + b));
+    for (int i = 0; i < TM; ++i) nw[i] = load_scales(wsbase + (sw[i] + b));
 #pragma unroll
-    for (int j = 0; j < TN; ++j) ndx[j] = load_scales(xsbase + (sx[j] + b));
+    for (int j = 0; j < TN; ++j) nx[j] = load_scales(xsbase + (sx[j] + b));
   };
   auto take_scales = [&](int st) {
-    const int b = st * kStageBlocks + 4 * h;
+    const int b = st * kStageBlocks + 8 * h;
 #pragma unroll
-    for (int i = 0; i < TM; ++i) dw[i] = shift_scales(ndw[i], b, a.nb);
+    for (int i = 0; i < TM; ++i) split_scales(shift_scales(nw[i], b, a.nb), dw[0][i], dw[1][i]);
 #pragma unroll
-    for (int j = 0; j < TN; ++j) dx[j] = shift_scales(ndx[j], b, a.nb);
+    for (int j = 0; j < TN; ++j) split_scales(shift_scales(nx[j], b, a.nb), dx[0][j], dx[1][j]);
   };
 
   f32x16 acc[TM][TN];
@@ -161,13 +173,13 @@ __global__ __launch_bounds__(64 * WM * WN, 1) void gemm_kernel(const GemmArgs a)
 #pragma unroll
     for (int i = 0; i < TM; ++i) A[S & 1][i] = *reinterpret_cast<const u32x4 *>(p + rw + i * (32 * kRowBytes));
   };
-  auto multiply = [&](auto s_c) {
-    constexpr int S = decltype(s_c)::value;
+  auto multiply = [&](auto s_c, auto buf_c) {
+    constexpr int S = decltype(s_c)::value, U = decltype(buf_c)::value;
 #pragma unroll
     for (int i = 0; i < TM; ++i)
 #pragma unroll
       for (int j = 0; j < TN; ++j)
-        acc[i][j] = mfma32<S>(A[S & 1][i], dw[i], B[S & 1][j], dx[j], acc[i][j]);
+        acc[i][j] = mfma32<S>(A[S & 1][i], dw[U][i], B[S & 1][j], dx[U][j], acc[i][j]);
   };
   // The next step's reads, then the copies where there are some, one at a time
   // between the matrix instructions of this step, so that none waits for another.
@@ -193,30 +205,32 @@ __global__ __launch_bounds__(64 * WM * WN, 1) void gemm_kernel(const GemmArgs a)
   // The copies of a stage are issued in the last step of the stage two before it
   // (the barrier there says that its buffer has been read) and in the step after.
   // Past the last stage they repeat it, into buffers that nobody reads any more, so
-  // that the loop is one straight line for the scheduler.
-  const int last = st1 - 1;
+  // that the loop is one straight line for the scheduler; its scales are zero there.
+  const int last = stages_all - 1;
   copy(st0, 0, kFirst, kLast);
   load_next_scales(st0);
   __builtin_amdgcn_s_waitcnt(0x0F70);  // vmcnt(0)
   __builtin_amdgcn_s_barrier();
-  take_scales(st0);
   copy(min(st0 + 1, last), 1, kFirst, kHalf);
-  load_next_scales(min(st0 + 1, last));
   read(0, s0);
-  for (int st = st0; st < st1; ++st) {
-    const int buf = (st - st0) & 1;
+  auto stage = [&](int st, auto buf_c) {
+    constexpr int buf = decltype(buf_c)::value;
+    if constexpr (buf == 0) {
+      take_scales(st);
+      load_next_scales(st + 2);
+    }
     __builtin_amdgcn_sched_barrier(0);
     read(buf, s1);
     copy(min(st + 1, last), buf ^ 1, kHalf, kLast);
-    multiply(s0);
+    multiply(s0, buf_c);
     interleave(kHalf);
     __builtin_amdgcn_sched_barrier(0);
     read(buf, s2);
-    multiply(s1);
+    multiply(s1, buf_c);
     interleave(s0);
     __builtin_amdgcn_sched_barrier(0);
     read(buf, s3);
-    multiply(s2);
+    multiply(s2, buf_c);
     interleave(s0);
     __builtin_amdgcn_sched_barrier(0);
     // The stage has been read (lgkmcnt), the next one's copies have landed (vmcnt).
@@ -225,11 +239,13 @@ __global__ __launch_bounds__(64 * WM * WN, 1) void gemm_kernel(const GemmArgs a)
     __builtin_amdgcn_sched_barrier(0);
     read(buf ^ 1, s0);
     copy(min(st + 2, last), buf, kFirst, kHalf);
-    multiply(s3);
+    multiply(s3, buf_c);
     interleave(kHalf);
     __builtin_amdgcn_sched_barrier(0);
-    take_scales(st + 1);
-    load_next_scales(min(st + 2, last));
+  };
+  for (int st = st0; st < st1; st += 2) {
+    stage(st, s0);
+    stage(st + 1, s1);
   }
   __builtin_amdgcn_s_waitcnt(0x0F70);  // no copy outlives the workgroup
 
@@ -293,7 +309,7 @@ GemmPlan gemm_plan(int64_t in_dim, int64_t out_dim, int64_t n_tok, size_t ws_byt
   const int64_t want = std::min<int64_t>(256 / std::max<int64_t>(tiles, 1), stages / 4);
   const int64_t fit = (int64_t)(ws_bytes / ((size_t)out_dim * n_tok * 4));
   p.splits = (int)std::max<int64_t>(1, std::min({want, fit, (int64_t)16}));
-  p.stages_per_split = (int)((stages + p.splits - 1) / p.splits);
+  p.stages_per_split = (int)((stages + p.splits - 1) / p.splits + 1) / 2 * 2;  // taken in twos
   p.splits = (int)((stages + p.stages_per_split - 1) / p.stages_per_split);
   return p;
 }
