@@ -77,9 +77,9 @@ size_t mxfp4_matmul_workspace_bytes(int64_t in_dim, int64_t out_dim, int64_t n_t
  * 2^-23 * sum |w x| before the rounding to out_type.  A NaN block makes every
  * output that uses it NaN.
  * n_tok == 0 or out_dim == 0 is a successful no-op.
- * Errors: in_dim % 32 != 0, in_dim == 0 or above 2^24 with work to do, out_dim
- * or n_tok above 2^31 - 1, negative sizes, unknown type, null pointers ->
- * Q8_0_EINVAL; codes or workspace not 16-byte aligned, out not aligned to its
+ * Errors: in_dim % 32 != 0, in_dim == 0 with work to do, in_dim above 2^24,
+ * out_dim or n_tok above 2^30, out_dim * n_tok above 2^38, negative sizes,
+ * unknown type, null pointers -> Q8_0_EINVAL; codes or workspace not 16-byte aligned, out not aligned to its
  * type -> Q8_0_EALIGN. */
 int mxfp4_matmul(void *out, int32_t out_type, const void *w_codes, const void *w_scales,
                  int64_t in_dim, int64_t out_dim, const void *x_codes, const void *x_scales,

@@ -35,15 +35,16 @@ int check_matrix(int64_t rows, int64_t k) {
   return Q8_0_OK;
 }
 
-// Sizes of a product: the kernels count blocks, rows and tokens in 32 bits.
-constexpr int64_t kMaxInDim = 1 << 24;
+// Sizes of a product: the kernels count blocks, rows, tokens and tiles in 32 bits.
+constexpr int64_t kMaxInDim = 1 << 24, kMaxRows = 1 << 30, kMaxOut = int64_t{1} << 38;
 int check_product(int64_t in_dim, int64_t out_dim, int64_t n_tok) {
   if (in_dim < 0 || out_dim < 0 || n_tok < 0 || in_dim % MXFP4_BLOCK_ELEMS != 0) return Q8_0_EINVAL;
-  if (in_dim > kMaxInDim || out_dim > INT32_MAX || n_tok > INT32_MAX) return Q8_0_EINVAL;
+  if (in_dim > kMaxInDim || out_dim > kMaxRows || n_tok > kMaxRows || out_dim * n_tok > kMaxOut)
+    return Q8_0_EINVAL;
   return Q8_0_OK;
 }
 
-bool use_gemm(int64_t in_dim, int64_t n_tok) { return n_tok > 64 && in_dim >= 256; }
+bool use_gemm(int64_t in_dim, int64_t n_tok) { return n_tok > 64 && in_dim >= 512; }
 
 int check_route(const float *logits, const float *bias, int64_t n_tok, int32_t n_expert,
                 int32_t n_used, int32_t scoring) {

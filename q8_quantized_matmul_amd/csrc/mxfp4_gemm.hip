@@ -7,16 +7,18 @@
 // turns, so the copies of the next one are in flight while one is multiplied,
 // with one barrier a stage.
 //
-// LDS: 128 bytes a row; the 16-byte block c of row r lies at position c ^ (r % 8),
+// LDS: 128 bytes a row; the 16-byte block c of row r lies at position c ^ (r / 2 % 8),
 // which the copies get by reading that block from memory (a lane's place in LDS
-// is fixed, its address in memory is not) and which makes the eight rows that are
-// read together use all banks once.
+// is fixed, its address in memory is not) and which makes sixteen rows that are
+// read together use all 64 banks once.
 //
 // A lane's block of instruction s (of a stage's four) is block 4 h + s, h its half,
-// so the four scale bytes it needs are one dword, the scale operand.  They go
-// straight to registers: scattered loads, a row each, that cost as many cache
-// lookups whatever they fetch, so a lane fetches eight bytes for two stages and
-// trades one dword with the lane of the other half.
+// so the four scale bytes it needs are one dword, the scale operand.  A row's scales
+// of a stage are eight bytes of a cache line that the copies push out of the first
+// cache before the next stage wants it, so they are fetched for four stages at once,
+// 32 bytes a row by two lanes, and shared by the waves through LDS (fetched by the
+// lanes that use them, a stage or two at a time, they were as many requests to the
+// second cache as the values).
 //
 // Blocks past the end of a row are read from inside the row and given the scale
 // byte 0 on both sides, whose products (below 2^-240) vanish in fp32; rows past
@@ -45,23 +47,41 @@ __device__ __forceinline__ void copy_to_lds(const uint8_t *src, uint8_t *dst) {
   __builtin_amdgcn_global_load_lds(src, dst, 16, 0, 0);
 }
 
-// Eight scale bytes at any address.  A lane reads those of blocks b..b+7, or, near
-// the end of a row of nb >= 8 blocks, of the row's last eight, and shifts them
-// down to b when it uses them (zero past the end).
-__device__ __forceinline__ uint64_t load_scales(const uint8_t *p) {
-  typedef uint64_t u64_a1 __attribute__((aligned(1)));
-  return *reinterpret_cast<const u64_a1 *>(p);
+// Sixteen scale bytes at any address.  A lane reads those of blocks b..b+15, or,
+// near the end of a row of nb >= 16 blocks, of the row's last sixteen, and shifts
+// them down to b when it uses them (zero past the end).
+struct Scales16 {
+  uint64_t lo, hi;
+};
+__device__ __forceinline__ Scales16 load_scales(const uint8_t *p) {
+  typedef uint32_t u32x4_a1 __attribute__((ext_vector_type(4), aligned(1)));
+  const u32x4_a1 v = *reinterpret_cast<const u32x4_a1 *>(p);
+  return {v.x | ((uint64_t)v.y << 32), v.z | ((uint64_t)v.w << 32)};
 }
-__device__ __forceinline__ uint64_t shift_scales(uint64_t v, int b, int nb) {
-  const int half = 4 * min(max(b + 8 - nb, 0), 8);  // bits; in two steps, so that 64 gives zero
-  return (v >> half) >> half;
+__device__ __forceinline__ u32x4 shift_scales(Scales16 v, int b, int nb) {
+  const int bytes = min(max(b + 16 - nb, 0), 16);
+  if (bytes >= 8) v = {v.hi, 0};
+  const int half = 4 * (bytes >= 8 ? bytes - 8 : bytes);  // bits; in two steps, so that 64 gives zero
+  const uint64_t lo = (v.lo >> half) >> half | (v.hi << (32 - half)) << (32 - half);
+  const uint64_t hi = (v.hi >> half) >> half;
+  return u32x4{(uint32_t)lo, (uint32_t)(lo >> 32), (uint32_t)hi, (uint32_t)(hi >> 32)};
 }
-// Half h of the wave holds the scales of blocks 8 h + 0..7 of its row's sixteen;
-// it needs blocks 4 h + 0..3 of the first eight (first) and of the last eight.
-__device__ __forceinline__ void split_scales(uint64_t v, uint32_t &first, uint32_t &second) {
-  const auto r = __builtin_amdgcn_permlane32_swap((uint32_t)v, (uint32_t)(v >> 32), false, false);
-  first = r[0];
-  second = r[1];
+// Waits until at most N of the wave's memory operations, and none of its LDS
+// operations, are outstanding.
+template <int N>
+__device__ __forceinline__ void wait_memory() {
+  static_assert(N < 64, "six bits");
+  __builtin_amdgcn_s_waitcnt((N & 15) | ((N >> 4) << 14) | (7 << 4));
+}
+// Half h of the wave holds dwords 4 h + 0..3 of its row's eight; stage u of the four
+// needs dword 2 u + h.
+__device__ __forceinline__ void split_scales(const u32x4 &v, uint32_t (&d)[4]) {
+  const auto p = __builtin_amdgcn_permlane32_swap(v.x, v.y, false, false);
+  const auto q = __builtin_amdgcn_permlane32_swap(v.z, v.w, false, false);
+  d[0] = p[0];
+  d[1] = q[0];
+  d[2] = p[1];
+  d[3] = q[1];
 }
 
 // Workgroups of one XCD (consecutive ids go round the eight) take neighbouring
@@ -83,12 +103,14 @@ __device__ __forceinline__ void tile_of(const GemmArgs &a, int &tn, int &tt, int
 }
 
 template <int WM, int WN, int TM, int TN, int TYPE>
-__global__ __launch_bounds__(64 * WM * WN, 1) void gemm_kernel(const GemmArgs a) {
-  constexpr int kW = WM * WN;
+__global__ __launch_bounds__(64 * WM * WN, WM * WN / 4) void gemm_kernel(const GemmArgs a) {
+  constexpr int kW = WM * WN, kThreads = 64 * kW;
   constexpr int BM = 32 * TM * WM, BN = 32 * TN * WN, ROWS = BM + BN;
   constexpr int COPIES = ROWS / 8 / kW;  // copy instructions of a wave per stage
-  static_assert(ROWS % (8 * kW) == 0 && BM % (8 * kW) == 0, "whole copies per wave and matrix");
+  constexpr int FETCHES = (ROWS * 2 + kThreads - 1) / kThreads;  // scale fetches of a thread per group
+  static_assert(ROWS % (8 * kW) == 0 && BM % (8 * kW) == 0 && kW % 2 == 0, "whole copies per wave and matrix");
   __shared__ __attribute__((aligned(16))) uint8_t lds[2][ROWS * kRowBytes];
+  __shared__ __attribute__((aligned(16))) uint8_t lds_scales[FETCHES * kThreads * 16];
 
   const int lane = threadIdx.x & 63;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
@@ -102,7 +124,7 @@ __global__ __launch_bounds__(64 * WM * WN, 1) void gemm_kernel(const GemmArgs a)
 
   // Copy i of the wave: rows 8 (wave + kW i) .. + 7 of the stage, weights first.
   const int lr = lane >> 3;
-  const int chunk = (lane & 7) ^ lr;
+  const int chunk = (lane & 7) ^ ((4 * (wave & 1) + (lr >> 1)) & 7);
   uint32_t off[COPIES];
 #pragma unroll
   for (int i = 0; i < COPIES; ++i) {
@@ -111,45 +133,59 @@ __global__ __launch_bounds__(64 * WM * WN, 1) void gemm_kernel(const GemmArgs a)
     off[i] = (uint32_t)at * (uint32_t)row_bytes;
   }
   const uint8_t *wbase = a.w + n0 * row_bytes, *xbase = a.x + t0 * row_bytes;
-  auto copy = [&](int st, int buf, auto from_c, auto to_c) {  // copies FROM..TO-1
+  auto copy = [&](int st, int buf) {
     const int b0 = st * kStageBlocks;
     const uint32_t c = (uint32_t)min(chunk, a.nb - 1 - b0) * 16u;
     const uint8_t *w = wbase + (int64_t)b0 * 16, *x = xbase + (int64_t)b0 * 16;
 #pragma unroll
-    for (int i = decltype(from_c)::value; i < decltype(to_c)::value; ++i) {
+    for (int i = 0; i < COPIES; ++i) {
       const uint8_t *src = (kW * i * 8 < BM ? w : x) + (off[i] + c);
       copy_to_lds(src, lds[buf] + (wave + kW * i) * 1024);
     }
   };
-  constexpr std::integral_constant<int, 0> kFirst{};
-  constexpr std::integral_constant<int, COPIES / 2> kHalf{};
-  constexpr std::integral_constant<int, COPIES> kLast{};
 
   const int wm = wave % WM, wn = wave / WM;
   const int lrow = lane & 31, h = lane >> 5;
+  // Scale fetch i of the thread: half (tid & 1) of the group's 32 bytes of a row.
   const uint8_t *wsbase = a.ws + (int64_t)n0 * a.nb, *xsbase = a.xs + (int64_t)t0 * a.nb;
-  uint32_t sw[TM], sx[TN];
+  const int sh = threadIdx.x & 1;
+  uint32_t soff[FETCHES];
 #pragma unroll
-  for (int i = 0; i < TM; ++i)
-    sw[i] = (uint32_t)(min(n0 + 32 * (wm * TM + i) + lrow, a.n - 1) - n0) * (uint32_t)a.nb;
+  for (int i = 0; i < FETCHES; ++i) {
+    const int r = min((int)threadIdx.x / 2 + i * (kThreads / 2), ROWS - 1);
+    const int at = r < BM ? min(n0 + r, a.n - 1) - n0 : min(t0 + r - BM, a.t - 1) - t0;
+    soff[i] = (uint32_t)at * (uint32_t)a.nb;
+  }
+  Scales16 fetched[FETCHES];
+  auto fetch_scales = [&](int st) {
+    const uint32_t b = (uint32_t)min(st * kStageBlocks + 16 * sh, a.nb - 16);
 #pragma unroll
-  for (int j = 0; j < TN; ++j)
-    sx[j] = (uint32_t)(min(t0 + 32 * (wn * TN + j) + lrow, a.t - 1) - t0) * (uint32_t)a.nb;
-  uint64_t nw[TM], nx[TN];              // scales of the next two stages
-  uint32_t dw[2][TM], dx[2][TN];        // of these two
-  auto load_next_scales = [&](int st) {
-    const uint32_t b = (uint32_t)min(st * kStageBlocks + 8 * h, a.nb - 8);
-#pragma unroll
-    for (int i = 0; i < TM; ++i) nw[i] = load_scales(wsbase + (sw[i] + b));
-#pragma unroll
-    for (int j = 0; j < TN; ++j) nx[j] = load_scales(xsbase + (sx[j] + b));
+    for (int i = 0; i < FETCHES; ++i) {
+      const bool isw = (int)threadIdx.x / 2 + i * (kThreads / 2) < BM;
+      fetched[i] = load_scales((isw ? wsbase : xsbase) + (soff[i] + b));
+    }
   };
-  auto take_scales = [&](int st) {
-    const int b = st * kStageBlocks + 8 * h;
+  auto share_scales = [&](int st) {
 #pragma unroll
-    for (int i = 0; i < TM; ++i) split_scales(shift_scales(nw[i], b, a.nb), dw[0][i], dw[1][i]);
+    for (int i = 0; i < FETCHES; ++i)  // the last may go past the rows, into padding
+      *reinterpret_cast<u32x4 *>(lds_scales + (threadIdx.x + i * kThreads) * 16) =
+          shift_scales(fetched[i], st * kStageBlocks + 16 * sh, a.nb);
+  };
+  u32x4 rw_s[TM], rx_s[TN];       // the next group's scales as read
+  uint32_t dw[TM][4], dx[TN][4];  // scale operands of the group's stages
+  auto read_scales = [&]() {
 #pragma unroll
-    for (int j = 0; j < TN; ++j) split_scales(shift_scales(nx[j], b, a.nb), dx[0][j], dx[1][j]);
+    for (int i = 0; i < TM; ++i)
+      rw_s[i] = *reinterpret_cast<const u32x4 *>(lds_scales + (32 * (wm * TM + i) + lrow) * 32 + h * 16);
+#pragma unroll
+    for (int j = 0; j < TN; ++j)
+      rx_s[j] = *reinterpret_cast<const u32x4 *>(lds_scales + (BM + 32 * (wn * TN + j) + lrow) * 32 + h * 16);
+  };
+  auto take_scales = [&]() {
+#pragma unroll
+    for (int i = 0; i < TM; ++i) split_scales(rw_s[i], dw[i]);
+#pragma unroll
+    for (int j = 0; j < TN; ++j) split_scales(rx_s[j], dx[j]);
   };
 
   f32x16 acc[TM][TN];
@@ -161,7 +197,7 @@ __global__ __launch_bounds__(64 * WM * WN, 1) void gemm_kernel(const GemmArgs a)
       for (int r = 0; r < 16; ++r) acc[i][j][r] = 0.0f;
 
   // Block 4 h + s of the lane's row, s = 0..3, in a 32-row tile.
-  const uint32_t rd = (uint32_t)lrow * kRowBytes + (uint32_t)(((4 * h) ^ (lane & 7)) * 16);
+  const uint32_t rd = (uint32_t)lrow * kRowBytes + (uint32_t)(((4 * h) ^ ((lrow >> 1) & 7)) * 16);
   const uint32_t rw = (uint32_t)wm * (TM * 32 * kRowBytes);
   const uint32_t rx = BM * kRowBytes + (uint32_t)wn * (TN * 32 * kRowBytes);
   u32x4 A[2][TM], B[2][TN];
@@ -173,81 +209,113 @@ __global__ __launch_bounds__(64 * WM * WN, 1) void gemm_kernel(const GemmArgs a)
 #pragma unroll
     for (int i = 0; i < TM; ++i) A[S & 1][i] = *reinterpret_cast<const u32x4 *>(p + rw + i * (32 * kRowBytes));
   };
-  auto multiply = [&](auto s_c, auto buf_c) {
-    constexpr int S = decltype(s_c)::value, U = decltype(buf_c)::value;
+  auto multiply = [&](auto s_c, auto u_c) {
+    constexpr int S = decltype(s_c)::value, U = decltype(u_c)::value;
 #pragma unroll
     for (int i = 0; i < TM; ++i)
 #pragma unroll
       for (int j = 0; j < TN; ++j)
-        acc[i][j] = mfma32<S>(A[S & 1][i], dw[U][i], B[S & 1][j], dx[U][j], acc[i][j]);
+        acc[i][j] = mfma32<S>(A[S & 1][i], dw[i][U], B[S & 1][j], dx[j][U], acc[i][j]);
   };
-  // The next step's reads, then the copies where there are some, one at a time
-  // between the matrix instructions of this step, so that none waits for another.
-  auto interleave = [&](auto copies_c) {
-    constexpr int kCopies = decltype(copies_c)::value, kMfma = TM * TN, kReads = TM + TN;
-    constexpr int kGap = kMfma / (kReads + kCopies) > 0 ? kMfma / (kReads + kCopies) : 1;
+  // With one wave a SIMD, whatever is issued between matrix instructions is free
+  // and whatever is issued between steps is not.  The next step's reads (and other
+  // LDS accesses), then the copies or scale fetches where there are some, go
+  // between the matrix instructions of this step, arithmetic over all of them.
+  auto interleave = [&](auto reads_c, auto memory_c, auto valu_c) {
+    constexpr int kReads = decltype(reads_c)::value, kMemory = decltype(memory_c)::value;
+    constexpr int kMfma = TM * TN, kAll = kReads + kMemory, kMost = (kAll + kMfma - 1) / kMfma;
+    constexpr int kValu = (decltype(valu_c)::value + kMfma - 1) / kMfma;
 #pragma unroll
-    for (int k = 0; k < kReads; ++k) {
-      __builtin_amdgcn_sched_group_barrier(0x100, 1, 0);     // LDS read
-      __builtin_amdgcn_sched_group_barrier(0x008, kGap, 0);  // matrix
-    }
+    for (int k = 0; k < kMfma; ++k) {
+      const int from = k * kAll / kMfma, to = (k + 1) * kAll / kMfma;
 #pragma unroll
-    for (int k = 0; k < kCopies; ++k) {
-      __builtin_amdgcn_sched_group_barrier(0x010, 1, 0);  // memory
-      __builtin_amdgcn_sched_group_barrier(0x008, kGap, 0);
+      for (int i = 0; i < kMost; ++i) {
+        if (from + i < to) {
+          if (from + i < kReads) __builtin_amdgcn_sched_group_barrier(0x080, 1, 0);  // LDS
+          else __builtin_amdgcn_sched_group_barrier(0x010, 1, 0);                    // memory
+        }
+      }
+      __builtin_amdgcn_sched_group_barrier(0x008, 1, 0);                     // matrix
+      if (kValu > 0) __builtin_amdgcn_sched_group_barrier(0x002, kValu, 0);  // arithmetic
     }
   };
   constexpr std::integral_constant<int, 0> s0{};
   constexpr std::integral_constant<int, 1> s1{};
   constexpr std::integral_constant<int, 2> s2{};
   constexpr std::integral_constant<int, 3> s3{};
+  constexpr std::integral_constant<int, TM + TN> kReads{};
+  constexpr std::integral_constant<int, 2 * (TM + TN)> kMoreReads{};
+  constexpr std::integral_constant<int, TM + TN + FETCHES> kReadsWrites{};
+  constexpr std::integral_constant<int, COPIES> kCopies{};
+  constexpr std::integral_constant<int, FETCHES> kFetches{};
+  constexpr std::integral_constant<int, 24 * FETCHES> kShifts{};
 
-  // The copies of a stage are issued in the last step of the stage two before it
-  // (the barrier there says that its buffer has been read) and in the step after.
-  // Past the last stage they repeat it, into buffers that nobody reads any more, so
-  // that the loop is one straight line for the scheduler; its scales are zero there.
+  // The copies of a stage are issued in the last step of the stage two before it: the
+  // barrier there says that its place has been read, and a whole stage passes until
+  // the next barrier waits for them.  Past the last stage they repeat it, into places
+  // that nobody reads any more, so that a stage is one straight line for the
+  // scheduler; its scales are zero there.  (A ring of four such stages, where it
+  // fits, is no faster: 4096 -> 2048 at 200 tokens 11.4 us with either.)
   const int last = stages_all - 1;
-  copy(st0, 0, kFirst, kLast);
-  load_next_scales(st0);
-  __builtin_amdgcn_s_waitcnt(0x0F70);  // vmcnt(0)
+  fetch_scales(st0);
+  copy(st0, 0);
+  copy(min(st0 + 1, last), 1);
+  share_scales(st0);
+  wait_memory<COPIES>();
   __builtin_amdgcn_s_barrier();
-  copy(min(st0 + 1, last), 1, kFirst, kHalf);
   read(0, s0);
-  auto stage = [&](int st, auto buf_c) {
-    constexpr int buf = decltype(buf_c)::value;
-    if constexpr (buf == 0) {
-      take_scales(st);
-      load_next_scales(st + 2);
-    }
+  read_scales();
+  // Stage u of a group of four: fetch the next group's scales, leave them in LDS (the
+  // group's own were read three barriers ago), read them.
+  auto stage = [&](int st, auto u_c) {
+    constexpr int U = decltype(u_c)::value, buf = U & 1;
     __builtin_amdgcn_sched_barrier(0);
     read(buf, s1);
-    copy(min(st + 1, last), buf ^ 1, kHalf, kLast);
-    multiply(s0, buf_c);
-    interleave(kHalf);
+    multiply(s0, u_c);
+    interleave(kReads, s0, s0);
     __builtin_amdgcn_sched_barrier(0);
     read(buf, s2);
-    multiply(s1, buf_c);
-    interleave(s0);
+    if constexpr (U == 0) fetch_scales(st + 4);
+    multiply(s1, u_c);
+    if constexpr (U == 0) interleave(kReads, kFetches, kFetches);
+    else interleave(kReads, s0, s0);
     __builtin_amdgcn_sched_barrier(0);
     read(buf, s3);
-    multiply(s2, buf_c);
-    interleave(s0);
+    if constexpr (U == 2) share_scales(st + 2);
+    multiply(s2, u_c);
+    if constexpr (U == 2) interleave(kReadsWrites, s0, kShifts);
+    else interleave(kReads, s0, s0);
     __builtin_amdgcn_sched_barrier(0);
-    // The stage has been read (lgkmcnt), the next one's copies have landed (vmcnt).
-    __builtin_amdgcn_s_waitcnt(0x0070);
+    // The stage has been read and the next one's copies have landed; a scale fetch,
+    // issued after them, may be outstanding.
+    wait_memory<(U == 0 ? FETCHES : 0)>();
     __builtin_amdgcn_s_barrier();
     __builtin_amdgcn_sched_barrier(0);
     read(buf ^ 1, s0);
-    copy(min(st + 2, last), buf, kFirst, kHalf);
-    multiply(s3, buf_c);
-    interleave(kHalf);
+    if constexpr (U == 3) read_scales();
+    copy(min(st + 2, last), buf);
+    multiply(s3, u_c);
+    if constexpr (U == 3) interleave(kMoreReads, kCopies, kCopies);
+    else interleave(kReads, kCopies, kCopies);
     __builtin_amdgcn_sched_barrier(0);
   };
-  for (int st = st0; st < st1; st += 2) {
+  // A last group of one or two stages is taken alone, but for the largest tile, whose
+  // registers leave no room for a second copy of the code: it multiplies zeros there.
+  constexpr bool kTail = TM * TN < 8;
+  int st = st0;
+  for (; st + (kTail ? 2 : 0) < st1; st += 4) {
+    take_scales();
+    stage(st, s0);
+    stage(st + 1, s1);
+    stage(st + 2, s2);
+    stage(st + 3, s3);
+  }
+  if (kTail && st < st1) {
+    take_scales();
     stage(st, s0);
     stage(st + 1, s1);
   }
-  __builtin_amdgcn_s_waitcnt(0x0F70);  // no copy outlives the workgroup
+  wait_memory<0>();  // no copy outlives the workgroup
 
   const int64_t base = (int64_t)ts * a.t * a.n;
 #pragma unroll
@@ -255,6 +323,7 @@ __global__ __launch_bounds__(64 * WM * WN, 1) void gemm_kernel(const GemmArgs a)
     const int t = t0 + 32 * (wn * TN + j) + lrow;
 #pragma unroll
     for (int i = 0; i < TM; ++i) {
+      __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
       for (int q = 0; q < 4; ++q) {
         const int o = n0 + 32 * (wm * TM + i) + 8 * q + 4 * h;
@@ -288,30 +357,53 @@ __global__ __launch_bounds__(256) void reduce_kernel(void *__restrict__ out, con
   }
 }
 
+// Tile shapes, and what a stage of 256 values takes when `at` workgroups share the
+// chip's 256 compute units (microseconds, measured; `slots` of them run at once).
 struct Tile {
-  int bm, bn;
+  int bm, bn, slots;
+  float us_full, us_half;  // at slots, at 256 workgroups
 };
-// Tile shapes, largest first.
-constexpr Tile kTiles[] = {{256, 256}, {256, 128}, {128, 128}, {128, 64}, {64, 64}};
+constexpr Tile kTiles[] = {{256, 256, 256, 1.6f, 1.6f},
+                           {128, 128, 512, 1.25f, 1.1f},
+                           {128, 64, 512, 0.95f, 0.8f},
+                           {64, 64, 1024, 1.0f, 0.5f}};
+constexpr int kNumTiles = 4, kMaxSplit = 16;
+// A split costs a launch and the partial sums' way to memory and back.
+constexpr float kSplitUs = 3.0f, kPartialBytesPerUs = 4.0e6f;
 
 }  // namespace
 
+// The tile and split of the smallest estimated time.  Large tiles read each row
+// fewer times, small ones give every compute unit work, and a split over K does
+// for long rows what small tiles do for many.  Measured, microseconds, chosen
+// first: 4096 -> 4096 at 4096 tokens 256^2 tiles 47, 128^2 54; 4096 -> 2048 at 4096
+// 128^2 30, 256^2 40; at 2048 128x64 19.7, 64^2 20.5, 128^2 21.9; at 1024 64^2 13.7,
+// 128x64 16.2; 32768 -> 1024 at 2048 128^2 in 4 splits 54, 256^2 in 8 63, 128x64 in 2
+// 61; 7168 -> 2048 at 129 64^2 in 4 splits 12.1, unsplit 17.7.
 GemmPlan gemm_plan(int64_t in_dim, int64_t out_dim, int64_t n_tok, size_t ws_bytes) {
-  GemmPlan p{};
   const int64_t stages = (in_dim / kBlock + kStageBlocks - 1) / kStageBlocks;
-  int64_t tiles = 0;
-  for (int i = 0; i < 5; ++i) {
-    p.tile = i;
-    tiles = ((out_dim + kTiles[i].bm - 1) / kTiles[i].bm) * ((n_tok + kTiles[i].bn - 1) / kTiles[i].bn);
-    if (tiles >= 256) break;
+  const double out_bytes = 4.0 * (double)out_dim * (double)n_tok;
+  GemmPlan best{};
+  double best_us = 0;
+  for (int i = 0; i < kNumTiles; ++i) {
+    const Tile &t = kTiles[i];
+    const int64_t tiles = ((out_dim + t.bm - 1) / t.bm) * ((n_tok + t.bn - 1) / t.bn);
+    for (int splits = 1; splits <= kMaxSplit; splits *= 2) {
+      if (splits > 1 && (stages < 4 * splits || tiles * splits > t.slots || splits * out_bytes > (double)ws_bytes)) break;
+      const double groups = (double)tiles * splits;
+      const double stage_us = groups <= 256 ? t.us_half : t.us_half + (t.us_full - t.us_half) * std::min(1.0, (groups - 256) / (t.slots - 256 + 1.0));
+      double us = std::max(1.0, groups / t.slots) * (double)stages / splits * stage_us;
+      if (splits > 1) us += kSplitUs + 2.0 * splits * out_bytes / kPartialBytesPerUs;
+      if ((i == 0 && splits == 1) || us < best_us) {
+        best_us = us;
+        best.tile = i;
+        best.splits = splits;
+      }
+    }
   }
-  p.splits = 1;
-  const int64_t want = std::min<int64_t>(256 / std::max<int64_t>(tiles, 1), stages / 4);
-  const int64_t fit = (int64_t)(ws_bytes / ((size_t)out_dim * n_tok * 4));
-  p.splits = (int)std::max<int64_t>(1, std::min({want, fit, (int64_t)16}));
-  p.stages_per_split = (int)((stages + p.splits - 1) / p.splits + 1) / 2 * 2;  // taken in twos
-  p.splits = (int)((stages + p.stages_per_split - 1) / p.stages_per_split);
-  return p;
+  best.stages_per_split = (int)((stages + best.splits - 1) / best.splits + 1) / 2 * 2;  // taken in twos
+  best.splits = (int)((stages + best.stages_per_split - 1) / best.stages_per_split);
+  return best;
 }
 
 size_t gemm_workspace_bytes(int64_t in_dim, int64_t out_dim, int64_t n_tok) {
@@ -337,10 +429,9 @@ hipError_t launch_gemm(const GemmPlan &p, void *out, int out_type, const uint8_t
   auto by_tile = [&](auto type_c) {
     constexpr int T = decltype(type_c)::value;
     switch (p.tile) {
-      case 0: return go(gemm_kernel<2, 2, 4, 4, T>, 256);
-      case 1: return go(gemm_kernel<2, 2, 4, 2, T>, 256);
-      case 2: return go(gemm_kernel<2, 2, 2, 2, T>, 256);
-      case 3: return go(gemm_kernel<2, 2, 2, 1, T>, 256);
+      case 0: return go(gemm_kernel<2, 4, 4, 2, T>, 512);
+      case 1: return go(gemm_kernel<2, 2, 2, 2, T>, 256);
+      case 2: return go(gemm_kernel<2, 2, 2, 1, T>, 256);
       default: return go(gemm_kernel<2, 2, 1, 1, T>, 256);
     }
   };

@@ -21,7 +21,7 @@ hipError_t launch_matmul(void *out, int out_type, const uint8_t *w, const uint8_
                          int64_t out_dim, const uint8_t *x, const uint8_t *xs, int64_t n_tok,
                          hipStream_t s);
 
-// mxfp4_gemm.hip: for many tokens.  in_dim >= 256 (a row's scales are read eight at a time).
+// mxfp4_gemm.hip: for many tokens.  in_dim >= 512 (a row's scales are read sixteen at a time).
 struct GemmPlan {
   int tile, splits, stages_per_split;
 };

@@ -70,7 +70,8 @@ def test_matmul_refusals(q8, lib):
     assert call(k=0) == q8.Q8_0_EINVAL
     assert call(k=(1 << 24) + 32) == q8.Q8_0_EINVAL
     assert call(n=-1) == q8.Q8_0_EINVAL
-    assert call(t=1 << 31) == q8.Q8_0_EINVAL
+    assert call(t=(1 << 30) + 1) == q8.Q8_0_EINVAL
+    assert call(n=1 << 20, t=1 << 19) == q8.Q8_0_EINVAL
     assert call(out_type=7) == q8.Q8_0_EINVAL
     for name in ("out", "wc", "ws", "xc", "xs"):
         assert call(**{name: None}) == q8.Q8_0_EINVAL
@@ -81,6 +82,16 @@ def test_matmul_refusals(q8, lib):
     assert call(work=FAKE + 8, nbytes=64) == q8.Q8_0_EALIGN
     assert call(t=0) == q8.Q8_0_OK
     assert call(n=0) == q8.Q8_0_OK
+
+
+def test_matmul_workspace(q8):
+    """Only long rows with too few tiles to fill the chip split, into whole partial outputs."""
+    size = q8.mxfp4_matmul_workspace_bytes
+    for k, n, t in ((4096, 2048, 1), (4096, 4096, 4096), (96, 64, 200), (64, 0, 100), (64, 64, 0), (33, 64, 64)):
+        assert size(k, n, t) == 0, (k, n, t)
+    assert size(32768, 1024, 2048) == 4 * 1024 * 2048 * 4
+    need = size(16384, 512, 100)
+    assert need > 0 and need % (512 * 100 * 4) == 0
 
 
 def test_topk_refusals(q8, lib):
