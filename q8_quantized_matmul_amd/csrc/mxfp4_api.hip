@@ -82,7 +82,7 @@ int run_layer(const mxfp4_moe_layer_args *a, void *workspace, size_t workspace_b
   for (const void *p : {a->gate_codes, a->up_codes, a->down_codes, a->x, (const void *)a->out})
     if (!aligned(p, 16)) return Q8_0_EALIGN;
   if (!aligned(a->selected, 4) || !aligned(a->weights, 4)) return Q8_0_EALIGN;
-  if (!workspace || workspace_bytes < mx::moe_layer_workspace_bytes(a->n_tok, a->n_used, a->n_expert, a->d_ff))
+  if (!workspace || workspace_bytes < mx::moe_layer_workspace_bytes(a->n_tok, a->n_used, a->n_expert, a->d_model, a->d_ff))
     return Q8_0_EWORKSPACE;
   if (!aligned(workspace, 256)) return Q8_0_EALIGN;
   if ((st = q8::check_device()) != Q8_0_OK) return st;
@@ -167,7 +167,7 @@ int moe_topk(int32_t *selected, float *weights, const float *logits, const float
 size_t mxfp4_moe_layer_workspace_bytes(int64_t n_tok, int32_t n_used, int32_t n_expert,
                                        int64_t d_model, int64_t d_ff) {
   if (!layer_sizes_ok(n_tok, n_used, n_expert, d_model, d_ff)) return 0;
-  return mx::moe_layer_workspace_bytes(n_tok, n_used, n_expert, d_ff);
+  return mx::moe_layer_workspace_bytes(n_tok, n_used, n_expert, d_model, d_ff);
 }
 
 int mxfp4_moe_layer(const mxfp4_moe_layer_args *args, void *workspace, size_t workspace_bytes,

@@ -51,7 +51,8 @@ struct MoeLayer {
   int32_t *selected;  // optional
   float *weights;     // optional
 };
-size_t moe_layer_workspace_bytes(int64_t n_tok, int32_t n_used, int32_t n_expert, int64_t d_ff);
+size_t moe_layer_workspace_bytes(int64_t n_tok, int32_t n_used, int32_t n_expert, int64_t d_model,
+                                 int64_t d_ff);
 hipError_t launch_moe_layer(const MoeLayer &m, uint8_t *ws, hipStream_t s);
 
 }  // namespace mx

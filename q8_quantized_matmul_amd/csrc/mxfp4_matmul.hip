@@ -25,25 +25,19 @@ struct MatmulArgs {
 };
 
 // NT: tiles of 16 tokens a workgroup takes.
-template <int NT, bool WHOLE, int TYPE>
+template <int NT, int KIND, int TYPE>
 __global__ __launch_bounds__(64 * kWaves) void stream_kernel(const MatmulArgs a) {
   __shared__ f32x4 part[kWaves * NT * 64];
-  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+  const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int kq = wave & (a.ks - 1), rt = wave / a.ks;
   const int tiles = kWaves / a.ks;  // row tiles of the workgroup
   const int row = lane & 15, g = lane >> 4;
   const int64_t o0 = ((int64_t)blockIdx.x * tiles + rt) * 16;
   const int64_t t0 = (int64_t)blockIdx.y * (16 * NT);
   // Rows past the ends are read as the last row; what they give is not stored.
-  const int64_t wr = min(o0 + row, a.n - 1);
-  const uint8_t *wc = a.w + wr * (a.nb * 16), *wsc = a.ws + wr * a.nb;
-  const uint8_t *xc[NT], *xsc[NT];
-#pragma unroll
-  for (int j = 0; j < NT; ++j) {
-    const int64_t xr = min(t0 + 16 * j + row, a.t - 1);
-    xc[j] = a.x + xr * (a.nb * 16);
-    xsc[j] = a.xs + xr * a.nb;
-  }
+  const uint8_t *wc = a.w + o0 * (a.nb * 16), *wsc = a.ws + o0 * a.nb;
+  const uint8_t *xc = a.x + t0 * (a.nb * 16), *xsc = a.xs + t0 * a.nb;
+  const uint32_t wr = (uint32_t)min<int64_t>(row, a.n - 1 - o0);
   f32x4 acc[NT];
 #pragma unroll
   for (int j = 0; j < NT; ++j) acc[j] = f32x4{0, 0, 0, 0};
@@ -53,9 +47,12 @@ __global__ __launch_bounds__(64 * kWaves) void stream_kernel(const MatmulArgs a)
     for (int s = kq; s < steps; s += a.ks) {
       const int b0 = s * kStepBlocks + 4 * g;
       Blocks4 A, B[NT];
-      load_blocks<WHOLE>(wc, wsc, b0, a.nb, A);
+      load_blocks<KIND>(wc, wsc, Offsets4<KIND>(wr, b0, a.nb), a.nb, A);
 #pragma unroll
-      for (int j = 0; j < NT; ++j) load_blocks<WHOLE>(xc[j], xsc[j], b0, a.nb, B[j]);
+      for (int j = 0; j < NT; ++j) {
+        const uint32_t xr = (uint32_t)min<int64_t>(16 * j + row, a.t - 1 - t0);
+        load_blocks<KIND>(xc, xsc, Offsets4<KIND>(xr, b0, a.nb), a.nb, B[j]);
+      }
 #pragma unroll
       for (int j = 0; j < NT; ++j) acc[j] = mfma_blocks4(A, B[j], acc[j]);
     }
@@ -79,8 +76,6 @@ __global__ __launch_bounds__(64 * kWaves) void stream_kernel(const MatmulArgs a)
   }
 }
 
-bool a4(const void *p) { return (reinterpret_cast<uintptr_t>(p) & 3) == 0; }
-
 }  // namespace
 
 hipError_t launch_matmul(void *out, int out_type, const uint8_t *w, const uint8_t *ws, int64_t in_dim,
@@ -90,27 +85,24 @@ hipError_t launch_matmul(void *out, int out_type, const uint8_t *w, const uint8_
   const int size = out_type == kF32 ? 4 : 2;
   MatmulArgs a{out, w, ws, x, xs, nb, out_dim, n_tok, 1, false};
   a.wide = out_dim % 4 == 0 && (reinterpret_cast<uintptr_t>(out) & (4 * size - 1)) == 0;
-  const bool whole = nb % 4 == 0 && a4(ws) && a4(xs);
   const int64_t tiles = (out_dim + 15) / 16, steps = (nb + kStepBlocks - 1) / kStepBlocks;
   const int nt = n_tok <= 16 ? 1 : n_tok <= 32 ? 2 : 4;
   while (a.ks < kWaves && a.ks < steps && tiles * a.ks < 4096) a.ks *= 2;
   const int64_t per_wg = kWaves / a.ks;
   const dim3 grid((uint32_t)((tiles + per_wg - 1) / per_wg), (uint32_t)((n_tok + 16 * nt - 1) / (16 * nt)));
   auto go = [&](auto kernel) { hipLaunchKernelGGL(kernel, grid, dim3(64 * kWaves), 0, s, a); };
-  auto by_type = [&](auto nt_c, auto whole_c) {
-    constexpr int NT = decltype(nt_c)::value;
-    constexpr bool W = decltype(whole_c)::value;
-    if (out_type == kF32) go(stream_kernel<NT, W, kF32>);
-    else if (out_type == kBF16) go(stream_kernel<NT, W, kBF16>);
-    else go(stream_kernel<NT, W, kF16>);
+  auto by_type = [&](auto nt_c, auto kind_c) {
+    constexpr int NT = decltype(nt_c)::value, K = decltype(kind_c)::value;
+    if (out_type == kF32) go(stream_kernel<NT, K, kF32>);
+    else if (out_type == kBF16) go(stream_kernel<NT, K, kBF16>);
+    else go(stream_kernel<NT, K, kF16>);
   };
-  auto by_nt = [&](auto whole_c) {
-    if (nt == 1) by_type(std::integral_constant<int, 1>{}, whole_c);
-    else if (nt == 2) by_type(std::integral_constant<int, 2>{}, whole_c);
-    else by_type(std::integral_constant<int, 4>{}, whole_c);
+  auto by_nt = [&](auto kind_c) {
+    if (nt == 1) by_type(std::integral_constant<int, 1>{}, kind_c);
+    else if (nt == 2) by_type(std::integral_constant<int, 2>{}, kind_c);
+    else by_type(std::integral_constant<int, 4>{}, kind_c);
   };
-  if (whole) by_nt(std::true_type{});
-  else by_nt(std::false_type{});
+  with_kind(nb, by_nt);
   return hipGetLastError();
 }
 

@@ -12,6 +12,8 @@
 // Products and scales are exact; sums are fp32.
 #pragma once
 
+#include <type_traits>
+
 #include "mxfp4_device.h"
 
 namespace mx {
@@ -44,37 +46,68 @@ struct Blocks4 {
 
 constexpr int kStepBlocks = 16;
 
+// How a matrix's rows end: kWhole, nb a multiple of 4, so four blocks are all inside
+// the row or all outside; kRagged, other nb of at least 4; kShort, nb below 4.
+constexpr int kWhole = 0, kRagged = 1, kShort = 2;
+inline int kind_of(int64_t nb) { return nb % 4 == 0 ? kWhole : nb > 4 ? kRagged : kShort; }
+// f(integral_constant of the kind of rows of nb blocks).
+template <typename F>
+inline void with_kind(int64_t nb, F f) {
+  const int k = kind_of(nb);
+  if (k == kWhole) f(std::integral_constant<int, kWhole>{});
+  else if (k == kRagged) f(std::integral_constant<int, kRagged>{});
+  else f(std::integral_constant<int, kShort>{});
+}
+
+// Blocks b0..b0+3 of row `row` of a matrix of nb blocks a row: byte offsets from the
+// matrix (rows and offsets within 32 bits: the caller gives the address of the tile
+// it works on, which is uniform, so that an address costs a lane one register).
+// Blocks outside the row are read from inside it, to keep the loads free of
+// branches, and given the scale byte 0; both operands do so, and products of 2^-254
+// vanish in fp32.  Scale rows may start at any byte.
+template <int KIND>
+struct Offsets4 {
+  uint32_t c[KIND == kWhole ? 1 : 4];
+  uint32_t s;
+  int past;  // blocks past the end, 0..4
+  __device__ __forceinline__ Offsets4(uint32_t row, int b0, int nb) {
+    past = min(max(b0 + 4 - nb, 0), 4);
+    s = row * (uint32_t)nb + (KIND == kShort ? 0u : (uint32_t)min(b0, nb - 4));
+    if constexpr (KIND == kWhole) {
+      c[0] = s * 16;
+    } else {
+#pragma unroll
+      for (int i = 0; i < 4; ++i) c[i] = (row * (uint32_t)nb + (uint32_t)min(b0 + i, nb - 1)) * 16;
+    }
+  }
+};
+
 // Global-memory pointers, also where the base came from memory: a generic load
 // would count on the LDS counter too.
 typedef __attribute__((address_space(1))) const u32x4 global_u32x4;
-typedef __attribute__((address_space(1))) const uint32_t global_u32;
 typedef __attribute__((address_space(1))) const uint8_t global_u8;
 
-// Blocks b0..b0+3 of a row of nb blocks; blocks past the row are zero (codes and
-// scale: 0 * 2^-127).  WHOLE: nb is a multiple of 4 and scale rows are dword
-// aligned, so the four blocks are all inside or all outside.
-template <bool WHOLE>
-__device__ __forceinline__ void load_blocks(const uint8_t *codes, const uint8_t *scales, int b0,
-                                            int nb, Blocks4 &r) {
-  if constexpr (WHOLE) {
-    if (b0 < nb) {
+template <int KIND>
+__device__ __forceinline__ void load_blocks(const uint8_t *codes, const uint8_t *scales,
+                                            const Offsets4<KIND> &o, int nb, Blocks4 &r) {
+  typedef uint32_t u32_a1 __attribute__((aligned(1)));
+  typedef __attribute__((address_space(1))) const u32_a1 global_u32_a1;
+  global_u8 *c = (global_u8 *)codes, *s = (global_u8 *)scales;
+  if constexpr (KIND == kWhole) {
 #pragma unroll
-      for (int i = 0; i < 4; ++i) r.c[i] = ((global_u32x4 *)(codes + (int64_t)b0 * 16))[i];
-      r.s = *(global_u32 *)(scales + b0);
-    } else {
-#pragma unroll
-      for (int i = 0; i < 4; ++i) r.c[i] = u32x4{0, 0, 0, 0};
-      r.s = 0;
-    }
+    for (int i = 0; i < 4; ++i) r.c[i] = ((global_u32x4 *)(c + o.c[0]))[i];
+    const uint32_t v = *(global_u32_a1 *)(s + o.s);
+    r.s = o.past ? 0u : v;
   } else {
-    r.s = 0;
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      r.c[i] = u32x4{0, 0, 0, 0};
-      if (b0 + i < nb) {
-        r.c[i] = ((global_u32x4 *)(codes + (int64_t)b0 * 16))[i];
-        r.s |= (uint32_t)((global_u8 *)scales)[b0 + i] << (8 * i);
-      }
+    for (int i = 0; i < 4; ++i) r.c[i] = *(global_u32x4 *)(c + o.c[i]);
+    if constexpr (KIND == kRagged) {  // near the end the four bytes read end with the row
+      const uint32_t v = *(global_u32_a1 *)(s + o.s);
+      r.s = (v >> (4 * o.past)) >> (4 * o.past);  // in two steps, so that 32 bits give zero
+    } else {
+      uint32_t v = 0;
+      for (int i = 0; i < nb; ++i) v |= (uint32_t)s[o.s + i] << (8 * i);
+      r.s = o.past == 4 ? 0u : v;
     }
   }
 }
