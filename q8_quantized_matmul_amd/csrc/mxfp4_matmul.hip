@@ -8,6 +8,8 @@
 // matrix core still takes weights ten times faster than memory gives them).
 // ks waves of a workgroup split a row's steps and are joined in LDS in wave
 // order, so that short rows and few rows still give the memory enough waves.
+#include <type_traits>
+
 #include "mxfp4_mfma.h"
 
 namespace mx {
@@ -25,7 +27,7 @@ struct MatmulArgs {
 };
 
 // NT: tiles of 16 tokens a workgroup takes.
-template <int NT, int KIND, int TYPE>
+template <int NT, bool SHORT, int TYPE>
 __global__ __launch_bounds__(64 * kWaves) void stream_kernel(const MatmulArgs a) {
   __shared__ f32x4 part[kWaves * NT * 64];
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
@@ -45,14 +47,16 @@ __global__ __launch_bounds__(64 * kWaves) void stream_kernel(const MatmulArgs a)
   const int steps = (a.nb + kStepBlocks - 1) / kStepBlocks;
   if (o0 < a.n) {
     for (int s = kq; s < steps; s += a.ks) {
-      const int b0 = s * kStepBlocks + 4 * g;
+      const int b0 = s * kStepBlocks;
       Blocks4 A, B[NT];
-      load_blocks<KIND>(wc, wsc, Offsets4<KIND>(wr, b0, a.nb), a.nb, A);
+      const Offsets4<SHORT> aw(wr, b0, a.nb);
+      load_blocks<SHORT>(wc, wsc, aw, a.nb, A);
 #pragma unroll
-      for (int j = 0; j < NT; ++j) {
-        const uint32_t xr = (uint32_t)min<int64_t>(16 * j + row, a.t - 1 - t0);
-        load_blocks<KIND>(xc, xsc, Offsets4<KIND>(xr, b0, a.nb), a.nb, B[j]);
-      }
+      for (int j = 0; j < NT; ++j)
+        load_blocks<SHORT>(xc, xsc, Offsets4<SHORT>((uint32_t)min<int64_t>(16 * j + row, a.t - 1 - t0), b0, a.nb), a.nb, B[j]);
+      finish_blocks(aw, A);
+#pragma unroll
+      for (int j = 0; j < NT; ++j) finish_blocks(aw, B[j]);
 #pragma unroll
       for (int j = 0; j < NT; ++j) acc[j] = mfma_blocks4(A, B[j], acc[j]);
     }
@@ -91,18 +95,20 @@ hipError_t launch_matmul(void *out, int out_type, const uint8_t *w, const uint8_
   const int64_t per_wg = kWaves / a.ks;
   const dim3 grid((uint32_t)((tiles + per_wg - 1) / per_wg), (uint32_t)((n_tok + 16 * nt - 1) / (16 * nt)));
   auto go = [&](auto kernel) { hipLaunchKernelGGL(kernel, grid, dim3(64 * kWaves), 0, s, a); };
-  auto by_type = [&](auto nt_c, auto kind_c) {
-    constexpr int NT = decltype(nt_c)::value, K = decltype(kind_c)::value;
-    if (out_type == kF32) go(stream_kernel<NT, K, kF32>);
-    else if (out_type == kBF16) go(stream_kernel<NT, K, kBF16>);
-    else go(stream_kernel<NT, K, kF16>);
+  auto by_type = [&](auto nt_c, auto short_c) {
+    constexpr int NT = decltype(nt_c)::value;
+    constexpr bool S = decltype(short_c)::value;
+    if (out_type == kF32) go(stream_kernel<NT, S, kF32>);
+    else if (out_type == kBF16) go(stream_kernel<NT, S, kBF16>);
+    else go(stream_kernel<NT, S, kF16>);
   };
-  auto by_nt = [&](auto kind_c) {
-    if (nt == 1) by_type(std::integral_constant<int, 1>{}, kind_c);
-    else if (nt == 2) by_type(std::integral_constant<int, 2>{}, kind_c);
-    else by_type(std::integral_constant<int, 4>{}, kind_c);
+  auto by_nt = [&](auto short_c) {
+    if (nt == 1) by_type(std::integral_constant<int, 1>{}, short_c);
+    else if (nt == 2) by_type(std::integral_constant<int, 2>{}, short_c);
+    else by_type(std::integral_constant<int, 4>{}, short_c);
   };
-  with_kind(nb, by_nt);
+  if (nb < 4) by_nt(std::true_type{});
+  else by_nt(std::false_type{});
   return hipGetLastError();
 }
 

@@ -12,8 +12,6 @@
 // Products and scales are exact; sums are fp32.
 #pragma once
 
-#include <type_traits>
-
 #include "mxfp4_device.h"
 
 namespace mx {
@@ -34,11 +32,12 @@ __device__ __forceinline__ f32x16 mfma32(const u32x4 &a, uint32_t sa, const u32x
   return __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(A, B, c, 4, 4, J, (int)sa, J, (int)sb);
 }
 
-// Four consecutive blocks of a row: a lane's operands of four instructions.  A
-// step of 16 blocks (512 values) gives lane group l / 16 blocks 4 * (l / 16) +
-// 0..3, so that the four lanes of a row read 256 adjacent bytes and the four
-// scale bytes are one dword; which k goes to which lane does not matter as long
-// as A and B agree.
+// A lane's operands of the four instructions of a step, 16 blocks (512 values) of a
+// row.  Instruction i takes blocks 4 i + g from lane group g = l / 16, so that the
+// four lanes of a row read 64 adjacent bytes at a time, what the caches serve at
+// once (four adjacent blocks to a lane: a layer of 64 tokens 546-559 us, with this
+// order 535; loads that bypass the caches 615).  Which k goes to which lane does
+// not matter as long as A and B agree.
 struct Blocks4 {
   u32x4 c[4];
   uint32_t s;  // scale of block i in byte i
@@ -46,39 +45,36 @@ struct Blocks4 {
 
 constexpr int kStepBlocks = 16;
 
-// How a matrix's rows end: kWhole, nb a multiple of 4, so four blocks are all inside
-// the row or all outside; kRagged, other nb of at least 4; kShort, nb below 4.
-constexpr int kWhole = 0, kRagged = 1, kShort = 2;
-inline int kind_of(int64_t nb) { return nb % 4 == 0 ? kWhole : nb > 4 ? kRagged : kShort; }
-// f(integral_constant of the kind of rows of nb blocks).
-template <typename F>
-inline void with_kind(int64_t nb, F f) {
-  const int k = kind_of(nb);
-  if (k == kWhole) f(std::integral_constant<int, kWhole>{});
-  else if (k == kRagged) f(std::integral_constant<int, kRagged>{});
-  else f(std::integral_constant<int, kShort>{});
+// The scale bytes of blocks 4 g .. 4 g + 3 in lane group g -- one dword of the row --
+// to byte i of lane group g = the scale of block 4 i + g: a 4 x 4 transpose of bytes
+// between the lane groups.
+__device__ __forceinline__ uint32_t spread_scales(uint32_t d) {
+  const uint32_t g = (threadIdx.x >> 4) & 3;
+  const auto h = __builtin_amdgcn_permlane32_swap(d, d, false, false);         // groups 0 1 0 1, 2 3 2 3
+  const auto lo = __builtin_amdgcn_permlane16_swap(h[0], h[0], false, false);  // group 0, 1 everywhere
+  const auto hi = __builtin_amdgcn_permlane16_swap(h[1], h[1], false, false);  // 2, 3
+  const uint32_t sel = g | ((4 + g) << 8);
+  return __builtin_amdgcn_perm(lo[1], lo[0], sel | 0x0C0C0000u) |
+         __builtin_amdgcn_perm(hi[1], hi[0], (sel << 16) | 0x0C0Cu);
 }
 
-// Blocks b0..b0+3 of row `row` of a matrix of nb blocks a row: byte offsets from the
-// matrix (rows and offsets within 32 bits: the caller gives the address of the tile
-// it works on, which is uniform, so that an address costs a lane one register).
-// Blocks outside the row are read from inside it, to keep the loads free of
+// Byte offsets of the lane's blocks b0 + 4 i + g of row `row` of a matrix of nb
+// blocks a row, from the matrix (within 32 bits: the caller gives the address of the
+// tile it works on, which is uniform, so that an address costs a lane one register).
+// Blocks past the end of the row are read from inside it, to keep the loads free of
 // branches, and given the scale byte 0; both operands do so, and products of 2^-254
-// vanish in fp32.  Scale rows may start at any byte.
-template <int KIND>
+// vanish in fp32.  Scale rows may start at any byte.  SHORT: nb below 4.
+template <bool SHORT>
 struct Offsets4 {
-  uint32_t c[KIND == kWhole ? 1 : 4];
+  uint32_t c[4];
   uint32_t s;
-  int past;  // blocks past the end, 0..4
+  int past;  // of the dword's four blocks b0 + 4 g .. + 3, those past the end
   __device__ __forceinline__ Offsets4(uint32_t row, int b0, int nb) {
-    past = min(max(b0 + 4 - nb, 0), 4);
-    s = row * (uint32_t)nb + (KIND == kShort ? 0u : (uint32_t)min(b0, nb - 4));
-    if constexpr (KIND == kWhole) {
-      c[0] = s * 16;
-    } else {
+    const int g = (threadIdx.x >> 4) & 3, b = b0 + 4 * g;
+    past = min(max(b + 4 - nb, 0), 4);
+    s = row * (uint32_t)nb + (SHORT ? 0u : (uint32_t)min(b, nb - 4));
 #pragma unroll
-      for (int i = 0; i < 4; ++i) c[i] = (row * (uint32_t)nb + (uint32_t)min(b0 + i, nb - 1)) * 16;
-    }
+    for (int i = 0; i < 4; ++i) c[i] = (row * (uint32_t)nb + (uint32_t)min(b0 + 4 * i + g, nb - 1)) * 16;
   }
 };
 
@@ -87,29 +83,27 @@ struct Offsets4 {
 typedef __attribute__((address_space(1))) const u32x4 global_u32x4;
 typedef __attribute__((address_space(1))) const uint8_t global_u8;
 
-template <int KIND>
+// The blocks, with their scales still as loaded: finish_blocks when they are used.
+template <bool SHORT>
 __device__ __forceinline__ void load_blocks(const uint8_t *codes, const uint8_t *scales,
-                                            const Offsets4<KIND> &o, int nb, Blocks4 &r) {
+                                            const Offsets4<SHORT> &o, int nb, Blocks4 &r) {
   typedef uint32_t u32_a1 __attribute__((aligned(1)));
   typedef __attribute__((address_space(1))) const u32_a1 global_u32_a1;
   global_u8 *c = (global_u8 *)codes, *s = (global_u8 *)scales;
-  if constexpr (KIND == kWhole) {
 #pragma unroll
-    for (int i = 0; i < 4; ++i) r.c[i] = ((global_u32x4 *)(c + o.c[0]))[i];
-    const uint32_t v = *(global_u32_a1 *)(s + o.s);
-    r.s = o.past ? 0u : v;
-  } else {
-#pragma unroll
-    for (int i = 0; i < 4; ++i) r.c[i] = *(global_u32x4 *)(c + o.c[i]);
-    if constexpr (KIND == kRagged) {  // near the end the four bytes read end with the row
-      const uint32_t v = *(global_u32_a1 *)(s + o.s);
-      r.s = (v >> (4 * o.past)) >> (4 * o.past);  // in two steps, so that 32 bits give zero
-    } else {
-      uint32_t v = 0;
-      for (int i = 0; i < nb; ++i) v |= (uint32_t)s[o.s + i] << (8 * i);
-      r.s = o.past == 4 ? 0u : v;
-    }
+  for (int i = 0; i < 4; ++i) r.c[i] = *(global_u32x4 *)(c + o.c[i]);
+  if constexpr (SHORT) {
+    r.s = 0;
+    for (int i = 0; i < nb; ++i) r.s |= (uint32_t)s[o.s + i] << (8 * i);
+  } else {  // near the end the four bytes read end with the row
+    r.s = *(global_u32_a1 *)(s + o.s);
   }
+}
+template <bool SHORT>
+__device__ __forceinline__ void finish_blocks(const Offsets4<SHORT> &o, Blocks4 &r) {
+  if constexpr (SHORT) r.s = o.past == 4 ? 0u : r.s;
+  else r.s = (r.s >> (4 * o.past)) >> (4 * o.past);  // in two steps, so that 32 bits give zero
+  r.s = spread_scales(r.s);
 }
 
 __device__ __forceinline__ f32x4 mfma_blocks4(const Blocks4 &a, const Blocks4 &b, f32x4 c) {

@@ -15,6 +15,7 @@
 // tokens share it (an expert with more than 16 reads them again, from the second
 // cache, for the next 16).
 #include <algorithm>
+#include <type_traits>
 
 #include "moe_topk.h"
 #include "mxfp4_mfma.h"
@@ -118,13 +119,14 @@ __global__ __launch_bounds__(256) void front_kernel(const Args a) {
 __host__ __device__ __forceinline__ int x_pitch(int d_model) { return d_model / 2 + 16; }
 __host__ __device__ __forceinline__ int x_scale_pitch(int d_model) { return (d_model / kBlock + 3) / 4 * 4 + 4; }
 
-// Blocks b0..b0+3 of a quantized x row in LDS, as load_blocks.
+// The lane's blocks of a step of a quantized x row in LDS, as load_blocks.
 __device__ __forceinline__ void load_x(const uint8_t *codes, const uint8_t *scales, int b0, int nb, Blocks4 &r) {
-  r.s = *reinterpret_cast<const uint32_t *>(scales + min(b0, (nb + 3) / 4 * 4 - 4));
-  const int over = min(max(b0 + 4 - nb, 0), 4);  // blocks past the row
-  r.s = over == 4 ? 0u : r.s & (0xFFFFFFFFu >> (8 * over));
+  const int g = (threadIdx.x >> 4) & 3, b = b0 + 4 * g;
+  const uint32_t s = *reinterpret_cast<const uint32_t *>(scales + min(b, (nb + 3) / 4 * 4 - 4));
+  const int past = min(max(b + 4 - nb, 0), 4);
+  r.s = spread_scales(past == 4 ? 0u : s & (0xFFFFFFFFu >> (8 * past)));
 #pragma unroll
-  for (int i = 0; i < 4; ++i) r.c[i] = *reinterpret_cast<const u32x4 *>(codes + min(b0 + i, nb - 1) * 16);
+  for (int i = 0; i < 4; ++i) r.c[i] = *reinterpret_cast<const u32x4 *>(codes + min(b0 + 4 * i + g, nb - 1) * 16);
 }
 
 // EPL: experts per lane of the router where this kernel routes, 0 where
@@ -132,8 +134,8 @@ __device__ __forceinline__ void load_x(const uint8_t *codes, const uint8_t *scal
 // 32 rows of d_ff (one block of mid) of one touched expert, gate and up together,
 // its eight waves splitting d_model.  128 registers, so that two workgroups share
 // a compute unit and one reads while the other joins its waves.
-template <int EPL, int KIND>
-__global__ __launch_bounds__(kThreads, KIND == kShort ? 2 : 4) void up_kernel(const Args a) {
+template <int EPL, bool SHORT>
+__global__ __launch_bounds__(kThreads, SHORT ? 2 : 4) void up_kernel(const Args a) {
   __shared__ uint32_t mask_lo[kMaxLayerExperts], mask_hi[kMaxLayerExperts];
   __shared__ int32_t touched[kMaxLayerExperts], first_of[kMaxLayerExperts];
   __shared__ int32_t n_touched;
@@ -146,17 +148,31 @@ __global__ __launch_bounds__(kThreads, KIND == kShort ? 2 : 4) void up_kernel(co
   const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
   const int n_expert = a.route.n_expert, n_used = a.route.n_used;
   uint8_t *xs_lds = x_lds + a.n_tok * x_pitch(a.d_model);
-  for (int e = tid; e < n_expert; e += kThreads) mask_lo[e] = mask_hi[e] = 0;
-  __syncthreads();
+  const bool single = EPL > 0 && a.n_tok == 1;  // its slots are the touched experts: no table to build
+  if (!single) {
+    for (int e = tid; e < n_expert; e += kThreads) mask_lo[e] = mask_hi[e] = 0;
+    __syncthreads();
+  }
   if constexpr (EPL > 0) {
     for (int t = wave; t < a.n_tok; t += kWaves) {
       int id;
       float w;
       route_token<EPL>(a.route, t, lane, id, w);
       if (lane < n_used) {
-        if (id >= 0) atomicOr(&mask_lo[id], 1u << t);
+        if (single && id >= 0) {
+          mask_lo[id] = 1;
+          mask_hi[id] = 0;
+          touched[lane] = id;
+          first_of[id] = lane;
+        } else if (id >= 0) {
+          atomicOr(&mask_lo[id], 1u << t);
+        }
         slot_id[t * n_used + lane] = id;
         slot_weight[t * n_used + lane] = w;
+      }
+      if (single) {
+        const uint64_t live = __ballot(lane < n_used && id >= 0);
+        if (lane == 0) n_touched = __popcll(live);
       }
     }
     quantize_x(a, 0, 1, x_lds, x_pitch(a.d_model), xs_lds, x_scale_pitch(a.d_model), tid, kThreads);
@@ -168,7 +184,7 @@ __global__ __launch_bounds__(kThreads, KIND == kShort ? 2 : 4) void up_kernel(co
   }
   __syncthreads();
   auto mask_of = [&](int e) { return ((uint64_t)mask_hi[e] << 32) | mask_lo[e]; };
-  if (wave == 0) {  // compact the touched experts, in order
+  if (!single && wave == 0) {  // compact the touched experts, in order
     int count = 0, pairs = 0;
     for (int e0 = 0; e0 < n_expert; e0 += 64) {
       const int e = e0 + lane;
@@ -191,7 +207,7 @@ __global__ __launch_bounds__(kThreads, KIND == kShort ? 2 : 4) void up_kernel(co
     }
     if (lane == 0) n_touched = count;
   }
-  __syncthreads();
+  if (!single) __syncthreads();
   const int count = n_touched;
 
   const int nb = a.d_model / kBlock, nbf = a.d_ff / kBlock;
@@ -202,8 +218,9 @@ __global__ __launch_bounds__(kThreads, KIND == kShort ? 2 : 4) void up_kernel(co
   for (int it = blockIdx.x; it < items; it += gridDim.x) {
     const int i = it / nbf, blk = it - i * nbf;
     const int e = __builtin_amdgcn_readfirstlane(touched[i]);
-    const uint64_t m = mask_of(e);
-    const int n = __builtin_amdgcn_readfirstlane(__popcll(m));
+    const uint64_t m = (uint64_t)(uint32_t)__builtin_amdgcn_readfirstlane((int)mask_hi[e]) << 32 |
+                       (uint32_t)__builtin_amdgcn_readfirstlane((int)mask_lo[e]);
+    const int n = __popcll(m);
     // Token of column c of tile j: the (16 j + c)-th set bit of the mask.
     const bool on = (m >> lane) & 1;
     const int column = __builtin_amdgcn_ds_permute(on ? 4 * bit_rank(m, lane) : 4 * 63, on ? lane : 0);
@@ -214,17 +231,23 @@ __global__ __launch_bounds__(kThreads, KIND == kShort ? 2 : 4) void up_kernel(co
 #pragma unroll
       for (int q = 0; q < 4; ++q) acc[q] = f32x4{0, 0, 0, 0};
       for (int s = wave; s < steps; s += kWaves) {
-        const int b0 = s * kStepBlocks + 4 * g;
+        const int b0 = s * kStepBlocks;
         Blocks4 A[4], B;
-        const Offsets4<KIND> off((uint32_t)row, b0, nb);
+        const Offsets4<SHORT> off((uint32_t)row, b0, nb);
 #pragma unroll
         for (int q = 0; q < 4; ++q) {
           const int64_t r = r0 + 16 * (q & 1);
-          load_blocks<KIND>((q < 2 ? a.gate : a.up) + r * (nb * 16), (q < 2 ? a.gate_s : a.up_s) + r * nb, off, nb, A[q]);
+          load_blocks<SHORT>((q < 2 ? a.gate : a.up) + r * (nb * 16), (q < 2 ? a.gate_s : a.up_s) + r * nb, off, nb, A[q]);
         }
         __builtin_amdgcn_sched_barrier(0);  // all weights are on their way before any is used
-        if constexpr (EPL > 0) load_x(x_lds + tok * x_pitch(a.d_model), xs_lds + tok * x_scale_pitch(a.d_model), b0, nb, B);
-        else load_blocks<KIND>(a.tab.x, a.tab.x_s, Offsets4<KIND>((uint32_t)tok, b0, nb), nb, B);
+        if constexpr (EPL > 0) {
+          load_x(x_lds + tok * x_pitch(a.d_model), xs_lds + tok * x_scale_pitch(a.d_model), b0, nb, B);
+        } else {
+          load_blocks<SHORT>(a.tab.x, a.tab.x_s, Offsets4<SHORT>((uint32_t)tok, b0, nb), nb, B);
+          finish_blocks(off, B);
+        }
+#pragma unroll
+        for (int q = 0; q < 4; ++q) finish_blocks(off, A[q]);
 #pragma unroll
         for (int q = 0; q < 4; ++q) acc[q] = mfma_blocks4(A[q], B, acc[q]);
       }
@@ -294,7 +317,7 @@ __global__ __launch_bounds__(kThreads, KIND == kShort ? 2 : 4) void up_kernel(co
 // hold different tokens, so no two add to one place), joined in wave order.
 constexpr int kAhead = 4;  // steps whose loads are issued together: 17 KB a wave
 
-template <int KIND, int TYPE>
+template <bool SHORT, int TYPE>
 __global__ __launch_bounds__(kThreads, 2) void down_kernel(const Args a) {
   extern __shared__ f32x4 sum[];  // [kWaves][n_tok][4]
   const int tid = threadIdx.x, lane = tid & 63;
@@ -322,15 +345,21 @@ __global__ __launch_bounds__(kThreads, 2) void down_kernel(const Args a) {
 #pragma unroll
         for (int u = 0; u < kAhead; ++u) {
           if (s + u < steps) {
-            const int b0 = (s + u) * kStepBlocks + 4 * g;
-            load_blocks<KIND>(wc, wsc, Offsets4<KIND>((uint32_t)row, b0, nb), nb, A[u]);
-            load_blocks<KIND>(a.tab.mid, a.tab.mid_s, Offsets4<KIND>((uint32_t)p, b0, nb), nb, B[u]);
+            const int b0 = (s + u) * kStepBlocks;
+            load_blocks<SHORT>(wc, wsc, Offsets4<SHORT>((uint32_t)row, b0, nb), nb, A[u]);
+            load_blocks<SHORT>(a.tab.mid, a.tab.mid_s, Offsets4<SHORT>((uint32_t)p, b0, nb), nb, B[u]);
           }
         }
         __builtin_amdgcn_sched_barrier(0);  // all of them are on their way before any is used
 #pragma unroll
-        for (int u = 0; u < kAhead; ++u)
-          if (s + u < steps) acc = mfma_blocks4(A[u], B[u], acc);
+        for (int u = 0; u < kAhead; ++u) {
+          if (s + u < steps) {
+            const Offsets4<SHORT> off(0, (s + u) * kStepBlocks, nb);
+            finish_blocks(off, A[u]);
+            finish_blocks(off, B[u]);
+            acc = mfma_blocks4(A[u], B[u], acc);
+          }
+        }
       }
       if (16 * j + row < at.n) {
         f32x4 &d = sum[(wave * a.n_tok + t) * 4 + g];
@@ -412,8 +441,8 @@ hipError_t launch_moe_layer(const MoeLayer &m, uint8_t *ws, hipStream_t s) {
   a.out = m.out;
 
   const size_t x_bytes = (size_t)m.n_tok * (x_pitch(a.d_model) + x_scale_pitch(a.d_model));
-  const bool fused = m.n_tok <= kFusedTok && x_bytes <= kFusedBytes;
-  const bool few = m.route->n_expert <= 256;
+  const bool few = m.route->n_expert <= 256;  // four experts a lane of the router
+  const bool fused = m.n_tok <= kFusedTok && few && x_bytes <= kFusedBytes;
   const int64_t touched = std::min<int64_t>(m.n_tok * m.route->n_used, m.route->n_expert);
   const dim3 grid1((uint32_t)std::min<int64_t>(touched * (m.d_ff / kBlock), kUpWorkgroups));
   const dim3 grid2((uint32_t)(m.d_model / 16));
@@ -426,22 +455,25 @@ hipError_t launch_moe_layer(const MoeLayer &m, uint8_t *ws, hipStream_t s) {
   auto up = [&](auto kernel) {
     hipLaunchKernelGGL(kernel, grid1, dim3(kThreads), fused ? x_bytes : 0, s, a);
   };
-  with_kind(m.d_model / kBlock, [&](auto kind_c) {
-    constexpr int K = decltype(kind_c)::value;
-    if (!fused) up(up_kernel<0, K>);
-    else if (few) up(up_kernel<4, K>);
-    else up(up_kernel<8, K>);
-  });
+  auto by_route = [&](auto short_c) {
+    constexpr bool S = decltype(short_c)::value;
+    if (!fused) up(up_kernel<0, S>);
+    else up(up_kernel<4, S>);
+  };
+  if (m.d_model / kBlock < 4) by_route(std::true_type{});
+  else by_route(std::false_type{});
   if ((err = hipGetLastError()) != hipSuccess) return err;
   auto down = [&](auto kernel) {
     hipLaunchKernelGGL(kernel, grid2, dim3(kThreads), (size_t)kWaves * m.n_tok * 64, s, a);
   };
-  with_kind(m.d_ff / kBlock, [&](auto kind_c) {
-    constexpr int K = decltype(kind_c)::value;
-    if (m.out_type == kF32) down(down_kernel<K, kF32>);
-    else if (m.out_type == kBF16) down(down_kernel<K, kBF16>);
-    else down(down_kernel<K, kF16>);
-  });
+  auto by_type = [&](auto short_c) {
+    constexpr bool S = decltype(short_c)::value;
+    if (m.out_type == kF32) down(down_kernel<S, kF32>);
+    else if (m.out_type == kBF16) down(down_kernel<S, kBF16>);
+    else down(down_kernel<S, kF16>);
+  };
+  if (m.d_ff / kBlock < 4) by_type(std::true_type{});
+  else by_type(std::false_type{});
   return hipGetLastError();
 }
 

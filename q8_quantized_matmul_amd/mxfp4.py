@@ -47,6 +47,7 @@ for _name, (_args, _res) in _sig.items():
     _fn.restype = _res
 
 EXPORTED = tuple(_sig)
+_calls = {_name: getattr(_lib, _name) for _name in EXPORTED}
 
 
 class Mxfp4(NamedTuple):
@@ -54,6 +55,12 @@ class Mxfp4(NamedTuple):
     even one in the low half) and e8m0 scale bytes uint8 [..., k/32]."""
     codes: torch.Tensor
     scales: torch.Tensor
+
+
+# A decode step makes these calls by the hundred: the raw forms of torch.cuda's
+# current device and stream cost a tenth of the public ones.
+_current_device = torch._C._cuda_getDevice
+_raw_stream = torch._C._cuda_getCurrentRawStream
 
 
 def _type(dtype, name: str) -> int:
@@ -80,29 +87,29 @@ def _device(t: torch.Tensor, name: str) -> torch.device:
 
 
 def _shape(t: torch.Tensor, name: str, *shape) -> None:
-    if tuple(t.shape) != shape:
+    if t.shape != shape:
         raise ValueError(f"{name} must have shape {list(shape)}, got {list(t.shape)}")
 
 
 def _matrix(m, name: str, device):
     """(codes pointer, scales pointer, leading shape, k) of an MXFP4 matrix."""
     codes, scales = m
-    k = 2 * codes.shape[-1]
-    if k % MXFP4_BLOCK_ELEMS != 0 or scales.shape != codes.shape[:-1] + (k // MXFP4_BLOCK_ELEMS,):
-        raise ValueError(f"{name}: codes {list(codes.shape)} and scales {list(scales.shape)} are "
-                         "not the two arrays of one matrix ([..., k/2] and [..., k/32])")
-    return (_ptr(codes, name + ".codes", torch.uint8, device),
-            _ptr(scales, name + ".scales", torch.uint8, device), codes.shape[:-1], k)
+    cs, ss = codes.shape, scales.shape
+    if len(cs) == 0 or len(ss) != len(cs) or cs[-1] != 16 * ss[-1] or cs[:-1] != ss[:-1]:
+        raise ValueError(f"{name}: codes {list(cs)} and scales {list(ss)} are not the two arrays of "
+                         "one matrix ([..., k/2] and [..., k/32])")
+    return (_ptr(codes, name, torch.uint8, device), _ptr(scales, name, torch.uint8, device),
+            cs[:-1], 2 * cs[-1])
 
 
 def _run(where: str, device, *args) -> None:
     """The C call with torch's current stream of `device` as its last argument."""
     index = device.index
-    if index == torch.cuda.current_device():
-        code = getattr(_lib, where)(*args, torch.cuda.current_stream(index).cuda_stream)
+    if index == _current_device():
+        code = _calls[where](*args, _raw_stream(index))
     else:
         with torch.cuda.device(index):
-            code = getattr(_lib, where)(*args, torch.cuda.current_stream(index).cuda_stream)
+            code = _calls[where](*args, _raw_stream(index))
     if code != 0:
         raise Q8Error(code, where)
 
@@ -117,8 +124,10 @@ def mxfp4_quantize(x: torch.Tensor, codes: torch.Tensor = None,
         raise ValueError("x must be [rows][k]")
     device = _device(x, "x")
     rows, k = x.shape
-    stride = x.stride(0) if rows > 1 else k
-    if k > 1 and x.stride(1) != 1:
+    stride, one = x.stride()
+    if rows <= 1:
+        stride = k
+    if one != 1 and k > 1:
         raise ValueError("the values of a row of x must be adjacent")
     if k % MXFP4_BLOCK_ELEMS != 0:
         raise ValueError("k must be a multiple of 32")
