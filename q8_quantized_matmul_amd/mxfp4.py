@@ -95,11 +95,13 @@ def _matrix(m, name: str, device):
     """(codes pointer, scales pointer, leading shape, k) of an MXFP4 matrix."""
     codes, scales = m
     cs, ss = codes.shape, scales.shape
-    if len(cs) == 0 or len(ss) != len(cs) or cs[-1] != 16 * ss[-1] or cs[:-1] != ss[:-1]:
+    if not cs or not ss or cs[-1] != 16 * ss[-1] or cs[:-1] != ss[:-1]:
         raise ValueError(f"{name}: codes {list(cs)} and scales {list(ss)} are not the two arrays of "
                          "one matrix ([..., k/2] and [..., k/32])")
-    return (_ptr(codes, name, torch.uint8, device), _ptr(scales, name, torch.uint8, device),
-            cs[:-1], 2 * cs[-1])
+    if not (codes.dtype == scales.dtype == torch.uint8 and codes.device == scales.device == device
+            and codes.is_contiguous() and scales.is_contiguous()):
+        raise ValueError(f"{name}: codes and scales must be contiguous uint8 on {device}")
+    return codes.data_ptr(), scales.data_ptr(), cs[:-1], 2 * cs[-1]
 
 
 def _run(where: str, device, *args) -> None:
@@ -135,11 +137,12 @@ def mxfp4_quantize(x: torch.Tensor, codes: torch.Tensor = None,
         codes = torch.empty((rows, k // 2), dtype=torch.uint8, device=device)
     if scales is None:
         scales = torch.empty((rows, k // MXFP4_BLOCK_ELEMS), dtype=torch.uint8, device=device)
-    c, s, lead, k_out = _matrix((codes, scales), "out", device)
-    if lead.numel() != rows or k_out != k:
+    out = Mxfp4(codes, scales)
+    c, s, lead, k_out = _matrix(out, "out", device)
+    if k_out != k or lead.numel() != rows:
         raise ValueError("codes and scales must hold as many rows and values as x")
     _run("mxfp4_quantize", device, c, s, x.data_ptr(), _type(x.dtype, "x"), stride, rows, k)
-    return Mxfp4(codes, scales)
+    return out
 
 
 def mxfp4_dequantize(m: Mxfp4, dtype: torch.dtype = torch.float32,
@@ -149,9 +152,12 @@ def mxfp4_dequantize(m: Mxfp4, dtype: torch.dtype = torch.float32,
     c, s, lead, k = _matrix(m, "m", device)
     if out is None:
         out = torch.empty((*lead, k), dtype=dtype, device=device)
-    _shape(out, "out", *lead, k)
-    _run("mxfp4_dequantize", device, _ptr(out, "out", out.dtype, device), _type(out.dtype, "out"),
-         c, s, lead.numel(), k)
+        o = out.data_ptr()
+    else:
+        _shape(out, "out", *lead, k)
+        dtype = out.dtype
+        o = _ptr(out, "out", dtype, device)
+    _run("mxfp4_dequantize", device, o, _type(dtype, "out"), c, s, lead.numel(), k)
     return out
 
 
@@ -189,12 +195,30 @@ def mxfp4_matmul(w: Mxfp4, x: Mxfp4, out: torch.Tensor = None,
     out_dim, n_tok = w_lead[0], x_lead[0]
     if out is None:
         out = torch.empty((n_tok, out_dim), dtype=out_dtype, device=device)
-    _shape(out, "out", n_tok, out_dim)
+        o = out.data_ptr()
+    else:
+        _shape(out, "out", n_tok, out_dim)
+        out_dtype = out.dtype
+        o = _ptr(out, "out", out_dtype, device)
     ws, ws_bytes, keep = _scratch(workspace, mxfp4_matmul_workspace_bytes(k, out_dim, n_tok)
                                   if workspace is None else 0, device)
-    _run("mxfp4_matmul", device, _ptr(out, "out", out.dtype, device), _type(out.dtype, "out"), wc,
-         wsc, k, out_dim, xc, xsc, n_tok, ws, ws_bytes)
+    _run("mxfp4_matmul", device, o, _type(out_dtype, "out"), wc, wsc, k, out_dim, xc, xsc, n_tok, ws,
+         ws_bytes)
     return out
+
+
+def _routing(selected, weights, n_tok: int, n_used: int, device):
+    """(selected, its pointer, weights, its pointer), allocated where not given."""
+    if selected is None:
+        selected = torch.empty((n_tok, n_used), dtype=torch.int32, device=device)
+    else:
+        _shape(selected, "selected", n_tok, n_used)
+    if weights is None:
+        weights = torch.empty((n_tok, n_used), dtype=torch.float32, device=device)
+    else:
+        _shape(weights, "weights", n_tok, n_used)
+    return (selected, _ptr(selected, "selected", torch.int32, device),
+            weights, _ptr(weights, "weights", torch.float32, device))
 
 
 def moe_topk(logits: torch.Tensor, n_used: int, bias: torch.Tensor = None,
@@ -207,19 +231,12 @@ def moe_topk(logits: torch.Tensor, n_used: int, bias: torch.Tensor = None,
         raise ValueError("logits must be [n_tok][n_expert]")
     device = _device(logits, "logits")
     n_tok, n_expert = logits.shape
-    if selected is None:
-        selected = torch.empty((n_tok, n_used), dtype=torch.int32, device=device)
-    if weights is None:
-        weights = torch.empty((n_tok, n_used), dtype=torch.float32, device=device)
-    _shape(selected, "selected", n_tok, n_used)
-    _shape(weights, "weights", n_tok, n_used)
+    selected, sp, weights, wp = _routing(selected, weights, n_tok, n_used, device)
     if bias is not None:
         _shape(bias, "bias", n_expert)
         bias = _ptr(bias, "bias", torch.float32, device)
-    _run("moe_topk", device, _ptr(selected, "selected", torch.int32, device),
-         _ptr(weights, "weights", torch.float32, device),
-         _ptr(logits, "logits", torch.float32, device), bias, n_tok, n_expert, n_used, scoring,
-         int(renormalize), scale)
+    _run("moe_topk", device, sp, wp, _ptr(logits, "logits", torch.float32, device), bias, n_tok,
+         n_expert, n_used, scoring, int(renormalize), scale)
     return selected, weights
 
 
@@ -264,13 +281,9 @@ def mxfp4_moe_layer(x: torch.Tensor, logits: torch.Tensor, gate: Mxfp4, up: Mxfp
         bias = _ptr(bias, "bias", torch.float32, device)
     if out is None:
         out = torch.empty((n_tok, d_model), dtype=out_dtype or x.dtype, device=device)
-    if selected is None:
-        selected = torch.empty((n_tok, n_used), dtype=torch.int32, device=device)
-    if weights is None:
-        weights = torch.empty((n_tok, n_used), dtype=torch.float32, device=device)
-    _shape(out, "out", n_tok, d_model)
-    _shape(selected, "selected", n_tok, n_used)
-    _shape(weights, "weights", n_tok, n_used)
+    else:
+        _shape(out, "out", n_tok, d_model)
+    selected, sp, weights, wp = _routing(selected, weights, n_tok, n_used, device)
     ws, ws_bytes, keep = _scratch(
         workspace, mxfp4_moe_layer_workspace_bytes(n_tok, n_used, n_expert, d_model, d_ff)
         if workspace is None else 0, device)
@@ -278,7 +291,6 @@ def mxfp4_moe_layer(x: torch.Tensor, logits: torch.Tensor, gate: Mxfp4, up: Mxfp
                         _type(out.dtype, "out"), _type(x.dtype, "x"),
                         _ptr(logits, "logits", torch.float32, device), bias, n_expert, n_used,
                         scoring, int(renormalize), scale, clamp, d_model, d_ff, n_tok, gc, gs, uc,
-                        us, dc, ds, _ptr(selected, "selected", torch.int32, device),
-                        _ptr(weights, "weights", torch.float32, device))
+                        us, dc, ds, sp, wp)
     _run("mxfp4_moe_layer", device, ctypes.byref(args), ws, ws_bytes)
     return out, selected, weights
