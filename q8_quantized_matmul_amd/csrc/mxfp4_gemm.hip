@@ -200,22 +200,27 @@ __global__ __launch_bounds__(64 * WM * WN, WM * WN / 4) void gemm_kernel(const G
   const uint32_t rd = (uint32_t)lrow * kRowBytes + (uint32_t)(((4 * h) ^ ((lrow >> 1) & 7)) * 16);
   const uint32_t rw = (uint32_t)wm * (TM * 32 * kRowBytes);
   const uint32_t rx = BM * kRowBytes + (uint32_t)wn * (TN * 32 * kRowBytes);
-  u32x4 A[2][TM], B[2][TN];
-  auto read = [&](int buf, auto s_c) {  // operands of instruction S of a stage
-    constexpr int S = decltype(s_c)::value;
+  // Two sets of operands: of the stage's instructions in turn, or, for small tiles, of
+  // this stage and the next, so that a stage waits for LDS once and not four times.
+  constexpr bool kSmall = TM * TN <= 4;
+  constexpr int kHeld = kSmall ? 4 : 1;
+  u32x4 A[2][kHeld][TM], B[2][kHeld][TN];
+  auto read = [&](int buf, auto s_c, auto set_c) {  // operands of instruction S of a stage
+    constexpr int S = decltype(s_c)::value, SET = decltype(set_c)::value, AT = kSmall ? S : 0;
     const uint8_t *p = lds[buf] + (rd ^ (S * 16));
 #pragma unroll
-    for (int j = 0; j < TN; ++j) B[S & 1][j] = *reinterpret_cast<const u32x4 *>(p + rx + j * (32 * kRowBytes));
+    for (int j = 0; j < TN; ++j) B[SET][AT][j] = *reinterpret_cast<const u32x4 *>(p + rx + j * (32 * kRowBytes));
 #pragma unroll
-    for (int i = 0; i < TM; ++i) A[S & 1][i] = *reinterpret_cast<const u32x4 *>(p + rw + i * (32 * kRowBytes));
+    for (int i = 0; i < TM; ++i) A[SET][AT][i] = *reinterpret_cast<const u32x4 *>(p + rw + i * (32 * kRowBytes));
   };
-  auto multiply = [&](auto s_c, auto u_c) {
+  auto multiply = [&](auto s_c, auto u_c, auto set_c) {
     constexpr int S = decltype(s_c)::value, U = decltype(u_c)::value;
+    constexpr int SET = decltype(set_c)::value, AT = kSmall ? S : 0;
 #pragma unroll
     for (int i = 0; i < TM; ++i)
 #pragma unroll
       for (int j = 0; j < TN; ++j)
-        acc[i][j] = mfma32<S>(A[S & 1][i], dw[i][U], B[S & 1][j], dx[j][U], acc[i][j]);
+        acc[i][j] = mfma32<S>(A[SET][AT][i], dw[i][U], B[SET][AT][j], dx[j][U], acc[i][j]);
   };
   // With one wave a SIMD, whatever is issued between matrix instructions is free
   // and whatever is issued between steps is not.  The next step's reads (and other
@@ -263,26 +268,54 @@ __global__ __launch_bounds__(64 * WM * WN, WM * WN / 4) void gemm_kernel(const G
   share_scales(st0);
   wait_memory<COPIES>();
   __builtin_amdgcn_s_barrier();
-  read(0, s0);
+  auto read_stage = [&](int buf, auto set_c) {
+    read(buf, s0, set_c);
+    read(buf, s1, set_c);
+    read(buf, s2, set_c);
+    read(buf, s3, set_c);
+  };
+  if constexpr (kSmall) read_stage(0, s0);
+  else read(0, s0, s0);
   read_scales();
-  // Stage u of a group of four: fetch the next group's scales, leave them in LDS (the
+  // Stage U of a group of four: fetch the next group's scales, leave them in LDS (the
   // group's own were read three barriers ago), read them.
-  auto stage = [&](int st, auto u_c) {
+  auto small_stage = [&](int st, auto u_c) {
+    constexpr int U = decltype(u_c)::value, buf = U & 1;
+    constexpr std::integral_constant<int, buf> now{};
+    constexpr std::integral_constant<int, buf ^ 1> next{};
+    // The stage is in registers and the next one's copies have landed; a scale fetch,
+    // issued after them, may be outstanding.
+    wait_memory<(U == 1 ? FETCHES : 0)>();
+    __builtin_amdgcn_s_barrier();
+    __builtin_amdgcn_sched_barrier(0);
+    read_stage(buf ^ 1, next);
+    if constexpr (U == 3) read_scales();
+    copy(min(st + 2, last), buf);
+    if constexpr (U == 0) fetch_scales(st + 4);
+    __builtin_amdgcn_sched_barrier(0);
+    multiply(s0, u_c, now);
+    multiply(s1, u_c, now);
+    multiply(s2, u_c, now);
+    multiply(s3, u_c, now);
+    if constexpr (U == 2) share_scales(st + 2);
+    __builtin_amdgcn_sched_barrier(0);
+  };
+  auto large_stage = [&](int st, auto u_c) {
     constexpr int U = decltype(u_c)::value, buf = U & 1;
     __builtin_amdgcn_sched_barrier(0);
-    read(buf, s1);
-    multiply(s0, u_c);
+    read(buf, s1, s1);
+    multiply(s0, u_c, s0);
     interleave(kReads, s0, s0);
     __builtin_amdgcn_sched_barrier(0);
-    read(buf, s2);
+    read(buf, s2, s0);
     if constexpr (U == 0) fetch_scales(st + 4);
-    multiply(s1, u_c);
+    multiply(s1, u_c, s1);
     if constexpr (U == 0) interleave(kReads, kFetches, kFetches);
     else interleave(kReads, s0, s0);
     __builtin_amdgcn_sched_barrier(0);
-    read(buf, s3);
+    read(buf, s3, s1);
     if constexpr (U == 2) share_scales(st + 2);
-    multiply(s2, u_c);
+    multiply(s2, u_c, s0);
     if constexpr (U == 2) interleave(kReadsWrites, s0, kShifts);
     else interleave(kReads, s0, s0);
     __builtin_amdgcn_sched_barrier(0);
@@ -291,17 +324,21 @@ __global__ __launch_bounds__(64 * WM * WN, WM * WN / 4) void gemm_kernel(const G
     wait_memory<(U == 0 ? FETCHES : 0)>();
     __builtin_amdgcn_s_barrier();
     __builtin_amdgcn_sched_barrier(0);
-    read(buf ^ 1, s0);
+    read(buf ^ 1, s0, s0);
     if constexpr (U == 3) read_scales();
     copy(min(st + 2, last), buf);
-    multiply(s3, u_c);
+    multiply(s3, u_c, s1);
     if constexpr (U == 3) interleave(kMoreReads, kCopies, kCopies);
     else interleave(kReads, kCopies, kCopies);
     __builtin_amdgcn_sched_barrier(0);
   };
+  auto stage = [&](int st, auto u_c) {
+    if constexpr (kSmall) small_stage(st, u_c);
+    else large_stage(st, u_c);
+  };
   // A last group of one or two stages is taken alone, but for the largest tile, whose
   // registers leave no room for a second copy of the code: it multiplies zeros there.
-  constexpr bool kTail = TM * TN < 8;
+  constexpr bool kTail = kSmall;
   int st = st0;
   for (; st + (kTail ? 2 : 0) < st1; st += 4) {
     take_scales();

@@ -26,9 +26,10 @@ struct MatmulArgs {
   bool wide;         // rows of out are aligned for stores of four values
 };
 
-// NT: tiles of 16 tokens a workgroup takes.
-template <int NT, bool SHORT, int TYPE>
-__global__ __launch_bounds__(64 * kWaves) void stream_kernel(const MatmulArgs a) {
+// NT: tiles of 16 tokens a workgroup takes.  AHEAD: steps of a wave whose loads are
+// issued together, for waves of several steps.
+template <int NT, int AHEAD, bool SHORT, int TYPE>
+__global__ __launch_bounds__(64 * kWaves, 2) void stream_kernel(const MatmulArgs a) {
   __shared__ f32x4 part[kWaves * NT * 64];
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int kq = wave & (a.ks - 1), rt = wave / a.ks;
@@ -46,19 +47,32 @@ __global__ __launch_bounds__(64 * kWaves) void stream_kernel(const MatmulArgs a)
 
   const int steps = (a.nb + kStepBlocks - 1) / kStepBlocks;
   if (o0 < a.n) {
-    for (int s = kq; s < steps; s += a.ks) {
-      const int b0 = s * kStepBlocks;
-      Blocks4 A, B[NT];
-      const Offsets4<SHORT> aw(wr, b0, a.nb);
-      load_blocks<SHORT>(wc, wsc, aw, a.nb, A);
+    for (int s = kq; s < steps; s += AHEAD * a.ks) {
+      Blocks4 A[AHEAD], B[AHEAD][NT];
 #pragma unroll
-      for (int j = 0; j < NT; ++j)
-        load_blocks<SHORT>(xc, xsc, Offsets4<SHORT>((uint32_t)min<int64_t>(16 * j + row, a.t - 1 - t0), b0, a.nb), a.nb, B[j]);
-      finish_blocks(aw, A);
+      for (int u = 0; u < AHEAD; ++u) {
+        const int b0 = (s + u * a.ks) * kStepBlocks;
+        if (u == 0 || b0 < a.nb) {
+          load_blocks<SHORT>(wc, wsc, Offsets4<SHORT>(wr, b0, a.nb), a.nb, A[u]);
 #pragma unroll
-      for (int j = 0; j < NT; ++j) finish_blocks(aw, B[j]);
+          for (int j = 0; j < NT; ++j)
+            load_blocks<SHORT>(xc, xsc, Offsets4<SHORT>((uint32_t)min<int64_t>(16 * j + row, a.t - 1 - t0), b0, a.nb), a.nb, B[u][j]);
+        }
+      }
+      __builtin_amdgcn_sched_barrier(0);  // all of them are on their way before any is used
 #pragma unroll
-      for (int j = 0; j < NT; ++j) acc[j] = mfma_blocks4(A, B[j], acc[j]);
+      for (int u = 0; u < AHEAD; ++u) {
+        const int b0 = (s + u * a.ks) * kStepBlocks;
+        if (u == 0 || b0 < a.nb) {
+          const Offsets4<SHORT> end(0, b0, a.nb);
+          finish_blocks(end, A[u]);
+#pragma unroll
+          for (int j = 0; j < NT; ++j) {
+            finish_blocks(end, B[u][j]);
+            acc[j] = mfma_blocks4(A[u], B[u][j], acc[j]);
+          }
+        }
+      }
     }
   }
   if (a.ks > 1) {
@@ -95,20 +109,27 @@ hipError_t launch_matmul(void *out, int out_type, const uint8_t *w, const uint8_
   const int64_t per_wg = kWaves / a.ks;
   const dim3 grid((uint32_t)((tiles + per_wg - 1) / per_wg), (uint32_t)((n_tok + 16 * nt - 1) / (16 * nt)));
   auto go = [&](auto kernel) { hipLaunchKernelGGL(kernel, grid, dim3(64 * kWaves), 0, s, a); };
-  auto by_type = [&](auto nt_c, auto short_c) {
-    constexpr int NT = decltype(nt_c)::value;
+  const bool ahead = steps > a.ks;
+  auto by_type = [&](auto nt_c, auto ahead_c, auto short_c) {
+    constexpr int NT = decltype(nt_c)::value, A = decltype(ahead_c)::value;
     constexpr bool S = decltype(short_c)::value;
-    if (out_type == kF32) go(stream_kernel<NT, S, kF32>);
-    else if (out_type == kBF16) go(stream_kernel<NT, S, kBF16>);
-    else go(stream_kernel<NT, S, kF16>);
+    if (out_type == kF32) go(stream_kernel<NT, A, S, kF32>);
+    else if (out_type == kBF16) go(stream_kernel<NT, A, S, kBF16>);
+    else go(stream_kernel<NT, A, S, kF16>);
   };
-  auto by_nt = [&](auto short_c) {
-    if (nt == 1) by_type(std::integral_constant<int, 1>{}, short_c);
-    else if (nt == 2) by_type(std::integral_constant<int, 2>{}, short_c);
-    else by_type(std::integral_constant<int, 4>{}, short_c);
+  constexpr std::integral_constant<int, 1> one{};
+  constexpr std::integral_constant<int, 2> two{};
+  constexpr std::integral_constant<int, 4> four{};
+  auto by_nt = [&](auto ahead_c, auto short_c) {
+    if (nt == 1) by_type(one, ahead_c, short_c);
+    else if (nt == 2) by_type(two, ahead_c, short_c);
+    else by_type(four, ahead_c, short_c);
   };
-  if (nb < 4) by_nt(std::true_type{});
-  else by_nt(std::false_type{});
+  if (nb < 4) by_nt(one, std::true_type{});
+  else if (!ahead) by_nt(one, std::false_type{});
+  else if (nt == 1) by_type(one, four, std::false_type{});
+  else if (nt == 2) by_type(two, two, std::false_type{});
+  else by_type(four, two, std::false_type{});
   return hipGetLastError();
 }
 
