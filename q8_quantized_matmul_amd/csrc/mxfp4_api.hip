@@ -44,7 +44,15 @@ int check_product(int64_t in_dim, int64_t out_dim, int64_t n_tok) {
   return Q8_0_OK;
 }
 
-bool use_gemm(int64_t in_dim, int64_t n_tok) { return n_tok > 64 && in_dim >= 512; }
+// The tiled kernel above 32 tokens; from 17 on where its stages are few or its rows
+// many; and never for rows of less than 512 values, whose scales it cannot fetch.
+// Measured (us, streaming / tiled): 4096 -> 2048 at 16 tokens 4.9 / 7.0, at 32 6.2 /
+// 7.0, at 64 8.5 / 6.8; 1024 -> 4096 at 32 6.1 / 4.2; 1024 -> 32768 at 32 10.1 / 7.3;
+// 32768 -> 1024 at 32 12.8 / 13.8, at 64 17.8 / 14.2.
+bool use_gemm(int64_t in_dim, int64_t out_dim, int64_t n_tok) {
+  if (in_dim < 512 || n_tok <= 16) return false;
+  return n_tok > 32 || in_dim <= 2048 || out_dim >= 8192;
+}
 
 int check_route(const float *logits, const float *bias, int64_t n_tok, int32_t n_expert,
                 int32_t n_used, int32_t scoring) {
@@ -128,7 +136,8 @@ int mxfp4_dequantize(void *out, int32_t out_type, const void *codes, const void 
 size_t mxfp4_matmul_workspace_bytes(int64_t in_dim, int64_t out_dim, int64_t n_tok) {
   if (check_product(in_dim, out_dim, n_tok) != Q8_0_OK || in_dim == 0 || out_dim == 0 || n_tok == 0)
     return 0;
-  return use_gemm(in_dim, n_tok) ? mx::gemm_workspace_bytes(in_dim, out_dim, n_tok) : 0;
+  return use_gemm(in_dim, out_dim, n_tok) ? mx::gemm_workspace_bytes(in_dim, out_dim, n_tok)
+                                          : mx::stream_workspace_bytes(in_dim, out_dim, n_tok);
 }
 
 int mxfp4_matmul(void *out, int32_t out_type, const void *w_codes, const void *w_scales,
@@ -144,12 +153,15 @@ int mxfp4_matmul(void *out, int32_t out_type, const void *w_codes, const void *w
   if ((st = q8::check_device()) != Q8_0_OK) return st;
   const auto *w = static_cast<const uint8_t *>(w_codes), *ws = static_cast<const uint8_t *>(w_scales);
   const auto *x = static_cast<const uint8_t *>(x_codes), *xs = static_cast<const uint8_t *>(x_scales);
-  if (use_gemm(in_dim, n_tok)) {
-    const mx::GemmPlan p = mx::gemm_plan(in_dim, out_dim, n_tok, workspace ? workspace_bytes : 0);
+  if (!workspace) workspace_bytes = 0;
+  if (use_gemm(in_dim, out_dim, n_tok)) {
+    const mx::GemmPlan p = mx::gemm_plan(in_dim, out_dim, n_tok, workspace_bytes);
     return status_of(mx::launch_gemm(p, out, out_type, w, ws, in_dim, out_dim, x, xs, n_tok,
                                      workspace, stream));
   }
-  return status_of(mx::launch_matmul(out, out_type, w, ws, in_dim, out_dim, x, xs, n_tok, stream));
+  const mx::StreamPlan p = mx::stream_plan(in_dim, out_dim, n_tok, workspace_bytes);
+  return status_of(mx::launch_stream(p, out, out_type, w, ws, in_dim, out_dim, x, xs, n_tok,
+                                     workspace, stream));
 }
 
 int moe_topk(int32_t *selected, float *weights, const float *logits, const float *bias,

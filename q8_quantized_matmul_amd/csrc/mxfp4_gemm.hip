@@ -102,14 +102,14 @@ __device__ __forceinline__ void tile_of(const GemmArgs &a, int &tn, int &tt, int
   tt = q / width;
 }
 
-template <int WM, int WN, int TM, int TN, int TYPE>
+template <int WM, int WN, int TM, int TN, int RING, int TYPE>
 __global__ __launch_bounds__(64 * WM * WN, WM * WN / 4) void gemm_kernel(const GemmArgs a) {
   constexpr int kW = WM * WN, kThreads = 64 * kW;
   constexpr int BM = 32 * TM * WM, BN = 32 * TN * WN, ROWS = BM + BN;
   constexpr int COPIES = ROWS / 8 / kW;  // copy instructions of a wave per stage
   constexpr int FETCHES = (ROWS * 2 + kThreads - 1) / kThreads;  // scale fetches of a thread per group
   static_assert(ROWS % (8 * kW) == 0 && BM % (8 * kW) == 0 && kW % 2 == 0, "whole copies per wave and matrix");
-  __shared__ __attribute__((aligned(16))) uint8_t lds[2][ROWS * kRowBytes];
+  __shared__ __attribute__((aligned(16))) uint8_t lds[RING][ROWS * kRowBytes];
   __shared__ __attribute__((aligned(16))) uint8_t lds_scales[FETCHES * kThreads * 16];
 
   const int lane = threadIdx.x & 63;
@@ -255,18 +255,16 @@ __global__ __launch_bounds__(64 * WM * WN, WM * WN / 4) void gemm_kernel(const G
   constexpr std::integral_constant<int, FETCHES> kFetches{};
   constexpr std::integral_constant<int, 24 * FETCHES> kShifts{};
 
-  // The copies of a stage are issued in the last step of the stage two before it: the
-  // barrier there says that its place has been read, and a whole stage passes until
-  // the next barrier waits for them.  Past the last stage they repeat it, into places
-  // that nobody reads any more, so that a stage is one straight line for the
-  // scheduler; its scales are zero there.  (A ring of four such stages, where it
-  // fits, is no faster: 4096 -> 2048 at 200 tokens 11.4 us with either.)
+  // The copies of a stage are issued in the stage RING before it, behind the barrier
+  // that says that its place has been read.  Past the last stage they repeat it, into
+  // places that nobody reads any more, so that a stage is one straight line for the
+  // scheduler; its scales are zero there.
   const int last = stages_all - 1;
   fetch_scales(st0);
-  copy(st0, 0);
-  copy(min(st0 + 1, last), 1);
+#pragma unroll
+  for (int r = 0; r < RING; ++r) copy(min(st0 + r, last), r);
   share_scales(st0);
-  wait_memory<COPIES>();
+  wait_memory<(RING - 1) * COPIES>();
   __builtin_amdgcn_s_barrier();
   auto read_stage = [&](int buf, auto set_c) {
     read(buf, s0, set_c);
@@ -280,17 +278,17 @@ __global__ __launch_bounds__(64 * WM * WN, WM * WN / 4) void gemm_kernel(const G
   // Stage U of a group of four: fetch the next group's scales, leave them in LDS (the
   // group's own were read three barriers ago), read them.
   auto small_stage = [&](int st, auto u_c) {
-    constexpr int U = decltype(u_c)::value, buf = U & 1;
-    constexpr std::integral_constant<int, buf> now{};
-    constexpr std::integral_constant<int, buf ^ 1> next{};
-    // The stage is in registers and the next one's copies have landed; a scale fetch,
-    // issued after them, may be outstanding.
-    wait_memory<(U == 1 ? FETCHES : 0)>();
+    constexpr int U = decltype(u_c)::value, buf = U % RING;
+    constexpr std::integral_constant<int, U & 1> now{};
+    constexpr std::integral_constant<int, (U & 1) ^ 1> next{};
+    // The stage is in registers and the next one's copies have landed; later copies and
+    // a scale fetch may be outstanding.
+    wait_memory<(RING - 2) * COPIES + (U >= 1 && U < RING ? FETCHES : 0)>();
     __builtin_amdgcn_s_barrier();
     __builtin_amdgcn_sched_barrier(0);
-    read_stage(buf ^ 1, next);
+    read_stage((buf + 1) % RING, next);
     if constexpr (U == 3) read_scales();
-    copy(min(st + 2, last), buf);
+    copy(min(st + RING, last), buf);
     if constexpr (U == 0) fetch_scales(st + 4);
     __builtin_amdgcn_sched_barrier(0);
     multiply(s0, u_c, now);
@@ -400,23 +398,23 @@ struct Tile {
   int bm, bn, slots;
   float us_full, us_half;  // at slots, at 256 workgroups
 };
-constexpr Tile kTiles[] = {{256, 256, 256, 1.6f, 1.6f},
+constexpr Tile kTiles[] = {{256, 256, 256, 1.55f, 1.55f},
                            {128, 128, 512, 1.25f, 1.1f},
-                           {128, 64, 512, 0.95f, 0.8f},
-                           {64, 64, 1024, 1.0f, 0.5f}};
+                           {128, 64, 512, 0.95f, 0.75f},
+                           {64, 64, 512, 0.65f, 0.4f}};
 constexpr int kNumTiles = 4, kMaxSplit = 16;
 // A split costs a launch and the partial sums' way to memory and back.
-constexpr float kSplitUs = 3.0f, kPartialBytesPerUs = 4.0e6f;
+constexpr float kSplitUs = 4.0f, kPartialBytesPerUs = 4.0e6f;
 
 }  // namespace
 
 // The tile and split of the smallest estimated time.  Large tiles read each row
 // fewer times, small ones give every compute unit work, and a split over K does
 // for long rows what small tiles do for many.  Measured, microseconds, chosen
-// first: 4096 -> 4096 at 4096 tokens 256^2 tiles 47, 128^2 54; 4096 -> 2048 at 4096
-// 128^2 30, 256^2 40; at 2048 128x64 19.7, 64^2 20.5, 128^2 21.9; at 1024 64^2 13.7,
-// 128x64 16.2; 32768 -> 1024 at 2048 128^2 in 4 splits 54, 256^2 in 8 63, 128x64 in 2
-// 61; 7168 -> 2048 at 129 64^2 in 4 splits 12.1, unsplit 17.7.
+// first: 4096 -> 4096 at 4096 tokens 256^2 tiles 46, 128^2 54; 4096 -> 2048 at 4096
+// 128^2 28, 256^2 40; at 2048 128x64 20, 64^2 23; at 1024 64^2 13.1, 128x64 15.1;
+// 32768 -> 1024 at 2048 128^2 in 4 splits 53, 256^2 in 8 63, 128x64 in 2 61; 7168 ->
+// 2048 at 129 64^2 in 2 splits 11.4, unsplit 13.2.
 GemmPlan gemm_plan(int64_t in_dim, int64_t out_dim, int64_t n_tok, size_t ws_bytes) {
   const int64_t stages = (in_dim / kBlock + kStageBlocks - 1) / kStageBlocks;
   const double out_bytes = 4.0 * (double)out_dim * (double)n_tok;
@@ -466,10 +464,10 @@ hipError_t launch_gemm(const GemmPlan &p, void *out, int out_type, const uint8_t
   auto by_tile = [&](auto type_c) {
     constexpr int T = decltype(type_c)::value;
     switch (p.tile) {
-      case 0: return go(gemm_kernel<2, 4, 4, 2, T>, 512);
-      case 1: return go(gemm_kernel<2, 2, 2, 2, T>, 256);
-      case 2: return go(gemm_kernel<2, 2, 2, 1, T>, 256);
-      default: return go(gemm_kernel<2, 2, 1, 1, T>, 256);
+      case 0: return go(gemm_kernel<2, 4, 4, 2, 2, T>, 512);
+      case 1: return go(gemm_kernel<2, 2, 2, 2, 2, T>, 256);
+      case 2: return go(gemm_kernel<2, 2, 2, 1, 2, T>, 256);
+      default: return go(gemm_kernel<2, 2, 1, 1, 4, T>, 256);
     }
   };
   if (type == kF32) by_tile(std::integral_constant<int, kF32>{});
@@ -477,14 +475,16 @@ hipError_t launch_gemm(const GemmPlan &p, void *out, int out_type, const uint8_t
   else by_tile(std::integral_constant<int, kF16>{});
   hipError_t err = hipGetLastError();
   if (err != hipSuccess || !split) return err;
-  const int64_t elems = out_dim * n_tok;
-  const dim3 rgrid((uint32_t)((elems + 1023) / 1024));
-  const float *part = static_cast<const float *>(workspace);
+  return launch_reduce(out, out_type, static_cast<const float *>(workspace), out_dim * n_tok, p.splits, s);
+}
+
+hipError_t launch_reduce(void *out, int out_type, const float *part, int64_t elems, int splits, hipStream_t s) {
+  const dim3 grid((uint32_t)((elems + 1023) / 1024));
   const bool wide = (reinterpret_cast<uintptr_t>(out) & (out_type == kF32 ? 15 : 7)) == 0;
-  auto red = [&](auto kernel) { hipLaunchKernelGGL(kernel, rgrid, dim3(256), 0, s, out, part, elems, p.splits, wide); };
-  if (out_type == kF32) red(reduce_kernel<kF32>);
-  else if (out_type == kBF16) red(reduce_kernel<kBF16>);
-  else red(reduce_kernel<kF16>);
+  auto go = [&](auto kernel) { hipLaunchKernelGGL(kernel, grid, dim3(256), 0, s, out, part, elems, splits, wide); };
+  if (out_type == kF32) go(reduce_kernel<kF32>);
+  else if (out_type == kBF16) go(reduce_kernel<kBF16>);
+  else go(reduce_kernel<kF16>);
   return hipGetLastError();
 }
 

@@ -16,10 +16,15 @@ hipError_t launch_quantize(uint8_t *codes, uint8_t *scales, const void *x, int x
 hipError_t launch_dequantize(void *out, int out_type, const uint8_t *codes, const uint8_t *scales,
                              int64_t n_rows, int64_t in_dim, hipStream_t s);
 
-// mxfp4_matmul.hip
-hipError_t launch_matmul(void *out, int out_type, const uint8_t *w, const uint8_t *ws, int64_t in_dim,
-                         int64_t out_dim, const uint8_t *x, const uint8_t *xs, int64_t n_tok,
-                         hipStream_t s);
+// mxfp4_matmul.hip: weight streaming, for few tokens.
+struct StreamPlan {
+  int ks, splits, steps_per_split;
+};
+StreamPlan stream_plan(int64_t in_dim, int64_t out_dim, int64_t n_tok, size_t ws_bytes);
+size_t stream_workspace_bytes(int64_t in_dim, int64_t out_dim, int64_t n_tok);
+hipError_t launch_stream(const StreamPlan &p, void *out, int out_type, const uint8_t *w,
+                         const uint8_t *ws, int64_t in_dim, int64_t out_dim, const uint8_t *x,
+                         const uint8_t *xs, int64_t n_tok, void *workspace, hipStream_t s);
 
 // mxfp4_gemm.hip: for many tokens.  in_dim >= 512 (a row's scales are read sixteen at a time).
 struct GemmPlan {
@@ -30,6 +35,9 @@ size_t gemm_workspace_bytes(int64_t in_dim, int64_t out_dim, int64_t n_tok);
 hipError_t launch_gemm(const GemmPlan &p, void *out, int out_type, const uint8_t *w, const uint8_t *ws,
                        int64_t in_dim, int64_t out_dim, const uint8_t *x, const uint8_t *xs,
                        int64_t n_tok, void *workspace, hipStream_t s);
+// out[i] = sum over s < splits, in order, of part[s * elems + i].
+hipError_t launch_reduce(void *out, int out_type, const float *part, int64_t elems, int splits,
+                         hipStream_t s);
 
 // moe_topk.hip
 struct RouteArgs;

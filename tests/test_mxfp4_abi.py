@@ -90,8 +90,9 @@ def test_matmul_workspace(q8):
     for k, n, t in ((4096, 2048, 1), (4096, 4096, 4096), (96, 64, 200), (64, 0, 100), (64, 64, 0), (33, 64, 64)):
         assert size(k, n, t) == 0, (k, n, t)
     assert size(32768, 1024, 2048) == 4 * 1024 * 2048 * 4
-    need = size(16384, 512, 100)
-    assert need > 0 and need % (512 * 100 * 4) == 0
+    for k, n, t in ((16384, 512, 100), (32768, 1024, 1), (32768, 40, 20)):
+        need = size(k, n, t)
+        assert need > 0 and need % (n * t * 4) == 0, (k, n, t)
 
 
 def test_topk_refusals(q8, lib):
