@@ -208,7 +208,7 @@ __global__ __launch_bounds__(kThreads, SHORT ? 2 : 4) void up_kernel(const Args 
     if (lane == 0) n_touched = count;
   }
   if (!single) __syncthreads();
-  const int count = n_touched;
+  const int count = __builtin_amdgcn_readfirstlane(n_touched);
 
   const int nb = a.d_model / kBlock, nbf = a.d_ff / kBlock;
   const int steps = (nb + kStepBlocks - 1) / kStepBlocks;
@@ -223,10 +223,12 @@ __global__ __launch_bounds__(kThreads, SHORT ? 2 : 4) void up_kernel(const Args 
     const int n = __popcll(m);
     // Token of column c of tile j: the (16 j + c)-th set bit of the mask.
     const bool on = (m >> lane) & 1;
-    const int column = __builtin_amdgcn_ds_permute(on ? 4 * bit_rank(m, lane) : 4 * 63, on ? lane : 0);
+    const int rank = __builtin_amdgcn_mbcnt_hi((uint32_t)(m >> 32), __builtin_amdgcn_mbcnt_lo((uint32_t)m, 0));
+    const int column = __builtin_amdgcn_ds_permute(on ? 4 * rank : 4 * 63, on ? lane : 0);
     const int64_t r0 = (int64_t)e * a.d_ff + blk * 32;
     for (int j = 0; 16 * j < n; ++j) {
-      const int tok = 16 * j + row < n ? __shfl(column, 16 * j + row, 64) : 0;  // idle columns: any row, not stored
+      const int of = __builtin_amdgcn_ds_bpermute(4 * (16 * j + row), column);
+      const int tok = 16 * j + row < n ? of : 0;  // idle columns: any row, not stored
       f32x4 acc[4];
 #pragma unroll
       for (int q = 0; q < 4; ++q) acc[q] = f32x4{0, 0, 0, 0};
@@ -277,11 +279,11 @@ __global__ __launch_bounds__(kThreads, SHORT ? 2 : 4) void up_kernel(const Args 
         const uint32_t byte = scale_byte(am);
         const uint32_t c = encode<kF32>(mid, byte);
         if (16 * j + row < n) {
-          const int64_t p = first_of[e] + 16 * j + row;
-          uint16_t *o = reinterpret_cast<uint16_t *>(a.tab.mid + p * (a.d_ff / 2) + blk * 16);
-          o[g] = (uint16_t)c;
-          o[4 + g] = (uint16_t)(c >> 16);
-          if (g == 0) a.tab.mid_s[p * nbf + blk] = (uint8_t)byte;
+          // 32 bits: at most 64 * 32 pairs of 2^15 blocks.
+          const uint32_t at = (uint32_t)(first_of[e] + 16 * j + row) * (uint32_t)nbf + (uint32_t)blk;
+          *reinterpret_cast<uint16_t *>(a.tab.mid + (at * 16 + 2 * g)) = (uint16_t)c;
+          *reinterpret_cast<uint16_t *>(a.tab.mid + (at * 16 + 2 * g + 8)) = (uint16_t)(c >> 16);
+          if (g == 0) a.tab.mid_s[at] = (uint8_t)byte;
         }
       }
       turn = (turn + 1) % kWaves;

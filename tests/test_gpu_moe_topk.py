@@ -77,6 +77,40 @@ def test_masked_experts_and_empty_rows(scoring):
     _check(z, 8, None, scoring, renormalize=False)
 
 
+@pytest.mark.parametrize("e,u", [(40, 8), (130, 8), (256, 32), (500, 5), (1024, 32)])
+@pytest.mark.parametrize("scoring", [0, 1, 2])
+def test_nearly_equal_scores(scoring, e, u):
+    """Logits a few steps of fp32 apart, logits whose sigmoid is 1, small scores far
+    apart as numbers but not as fp32 sums, and a bias that makes them all one."""
+    g = torch.Generator(device="cuda").manual_seed(e + u + scoring)
+    step = torch.randint(0, 40, (6, e), generator=g, device="cuda").float()
+    z = 1 + step * 2.0 ** -23
+    z[1] = 38 + step[1]
+    z[2] = -70 - step[2] / 4
+    z[3] = -70 - torch.rand((e,), generator=g, device="cuda") * 10
+    z[4] = -step[4] * 2.0 ** -140  # subnormal
+    z[5, e // 3:] = -float("inf")
+    _check(z, u, None, scoring)
+    _check(z, u, torch.full((e,), 3.0, device="cuda"), scoring)
+    b = torch.randn((e,), generator=g, device="cuda")
+    b[1::3] = 1e30
+    b[2::7] = -1e30
+    _check(z, u, b, scoring)
+
+
+def test_infinite_and_nan_biases():
+    z = torch.randn((5, 300), device="cuda")
+    b = torch.zeros(300, device="cuda")
+    b[7] = b[290] = float("inf")
+    b[11] = float("nan")
+    b[20:200] = -float("inf")
+    for scoring in (0, 1, 2):
+        sel, _ = _q8().moe_topk(z, 6, bias=b, scoring=scoring)
+        ids, _ = ref.route(z.cpu().numpy(), 6, b.cpu().numpy(), scoring)
+        assert np.array_equal(sel.cpu().numpy(), ids)
+        assert (sel[:, :3] == torch.tensor([11, 7, 290], device="cuda")).all()
+
+
 @pytest.mark.parametrize("renormalize", [True, False])
 @pytest.mark.parametrize("scoring", [0, 1, 2])
 def test_nan_and_infinite_logits(scoring, renormalize):
