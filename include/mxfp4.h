@@ -146,14 +146,15 @@ typedef struct mxfp4_moe_layer_args {
     float *weights;          /* optional fp32 [n_tok][n_used]: moe_topk's weights    */
 } mxfp4_moe_layer_args;
 
-/* Workspace bytes mxfp4_moe_layer needs (routing tables and the quantized mid
- * of every pair); 0 for sizes it refuses. */
+/* Workspace bytes mxfp4_moe_layer needs (routing tables, the quantized x and the
+ * quantized mid of every pair); 0 for sizes it refuses. */
 size_t mxfp4_moe_layer_workspace_bytes(int64_t n_tok, int32_t n_used, int32_t n_expert,
                                        int64_t d_model, int64_t d_ff);
 
 /* The whole MoE layer for a few tokens, from router logits to the weighted sum
- * of the experts, in two kernels (q8_0_moe_ffn is its 8-bit counterpart from
- * given ids on).  For token t, with (e_j, w_j) = moe_topk of its logits:
+ * of the experts, in two kernels up to eight tokens (and 256 experts, and
+ * n_tok * d_model about 2^16) and three above (q8_0_moe_ffn is its 8-bit
+ * counterpart from given ids on).  For token t, with (e_j, w_j) = moe_topk of its logits:
  *   x4    = mxfp4_quantize(x_t)
  *   gate  = W_gate[e_j] x4, up = W_up[e_j] x4          (products as mxfp4_matmul)
  *   mid   = silu(gate) * up, silu(g) = g / (1 + exp(-g)), after the optional

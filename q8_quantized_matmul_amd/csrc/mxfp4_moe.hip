@@ -3,12 +3,16 @@
 //                quantize mid;
 //   down_kernel  down of every pair, weighted sum over a token's experts.
 // At these sizes the layer is bound by reading each touched expert's matrices
-// once (17 bytes per 32 weights), and at one token by latency, so with up to four
-// tokens routing and quantizing are not launches of their own: every workgroup of
-// the first kernel does both for itself (a wave per token, moe_topk.h; x in LDS).
-// With more tokens a small kernel in front does it once (4096 x 2048, 4 of 64
-// experts: 19.5 us fused and 21.9 with the front kernel at 1 token, 55.4 and 56.0
-// at 4, 74.8 and 74.2 at 6, 123 and 116 at 16).
+// once (17 bytes per 32 weights), and at a few tokens by latency, so with up to
+// eight, a wave each, routing and quantizing are not launches of their own: every
+// workgroup of the first kernel does both for itself (moe_topk.h; x in LDS).  With
+// more tokens a small kernel in front does it once.  2048 x 768, 6 of 64 experts,
+// fused and with the front kernel: 31.2 and 32.2 us at 5 tokens, 39.3 and 38.0 at 8
+// (whose launch costs the caller 3 us more), 45.5 and 40.0 at 11.
+//
+// Measured, 4096 x 2048, 8 of 256 experts: one token 26.8 us (107 MB, 4.0 TB/s:
+// launches, routing and the tables' chain are 8 us of it), 64 tokens 527 us (3.0 GB
+// of 222 experts, 5.6 TB/s of the 5.9 that reading alone reaches).
 //
 // A touched expert's tokens are the columns of 16x16x128 matrix instructions
 // (mxfp4_mfma.h), 16 of them a tile, so its weights are read once however many
@@ -25,7 +29,7 @@ namespace {
 
 constexpr int kWaves = 8;
 constexpr int kThreads = 64 * kWaves;
-constexpr int kFusedTok = 4;              // up to here up_kernel routes and quantizes
+constexpr int kFusedTok = kWaves;         // up to here up_kernel routes and quantizes
 constexpr size_t kFusedBytes = 36 * 1024;  // ... if x fits beside the rest of two workgroups' LDS
 constexpr int64_t kUpWorkgroups = 512;     // two a compute unit
 
@@ -175,7 +179,12 @@ __global__ __launch_bounds__(kThreads, SHORT ? 2 : 4) void up_kernel(const Args 
         if (lane == 0) n_touched = __popcll(live);
       }
     }
-    quantize_x(a, 0, 1, x_lds, x_pitch(a.d_model), xs_lds, x_scale_pitch(a.d_model), tid, kThreads);
+    // The waves that do not route, if half of them are free; else all.
+    const int busy = a.n_tok <= kWaves / 2 ? a.n_tok : 0;
+    if (wave >= busy) {
+      quantize_x(a, 0, 1, x_lds, x_pitch(a.d_model), xs_lds, x_scale_pitch(a.d_model), tid - 64 * busy,
+                 kThreads - 64 * busy);
+    }
   } else {
     for (int p = tid; p < a.n_tok * n_used; p += kThreads) {
       const int id = a.selected[p], t = p / n_used;
