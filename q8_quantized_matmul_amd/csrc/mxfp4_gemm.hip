@@ -3,9 +3,16 @@
 //
 // A workgroup of WM x WN waves computes 32 TM WM weight rows x 32 TN WN tokens.
 // A stage is 256 values of every row, one 128-byte line: the copies go straight
-// from memory to LDS, 1 KB (eight rows) an instruction, and two stages take
-// turns, so the copies of the next one are in flight while one is multiplied,
-// with one barrier a stage.
+// from memory to LDS, 1 KB (eight rows) an instruction, into the RING places that
+// stages take in turn, so the copies of the next ones are in flight while one is
+// multiplied, with one barrier a stage.
+//
+// What bounds it: 256 workgroups of 256^2 tiles take 1.55 us a stage, of which the
+// copies alone are 1.3 (the second caches' rate) and the matrix instructions alone
+// 1.34 (6.4 PFLOP/s, what the chip holds on random values for its power; 9.6 on
+// constant ones); then the stores and the join of the splits.  8192^3 311 us, 3.5
+// PFLOP/s; 32768 -> 1024 at 2048 tokens 48 us and 7 for the join; 4096 -> 2048 at
+// 200 9.2 us, two thirds of it launch, first loads and stores.
 //
 // LDS: 128 bytes a row; the 16-byte block c of row r lies at position c ^ (r / 2 % 8),
 // which the copies get by reading that block from memory (a lane's place in LDS
@@ -17,8 +24,7 @@
 // of a stage are eight bytes of a cache line that the copies push out of the first
 // cache before the next stage wants it, so they are fetched for four stages at once,
 // 32 bytes a row by two lanes, and shared by the waves through LDS (fetched by the
-// lanes that use them, a stage or two at a time, they were as many requests to the
-// second cache as the values).
+// lanes that use them, two stages at a time: 8192^3 335 us for 311).
 //
 // Blocks past the end of a row are read from inside the row and given the scale
 // byte 0 on both sides, whose products (below 2^-240) vanish in fp32; rows past
@@ -336,6 +342,7 @@ __global__ __launch_bounds__(64 * WM * WN, WM * WN / 4) void gemm_kernel(const G
   };
   // A last group of one or two stages is taken alone, but for the largest tile, whose
   // registers leave no room for a second copy of the code: it multiplies zeros there.
+  // gemm_plan gives a split whole pairs, or whole fours, so no split takes the next one's.
   constexpr bool kTail = kSmall;
   int st = st0;
   for (; st + (kTail ? 2 : 0) < st1; st += 4) {
@@ -423,21 +430,23 @@ GemmPlan gemm_plan(int64_t in_dim, int64_t out_dim, int64_t n_tok, size_t ws_byt
   for (int i = 0; i < kNumTiles; ++i) {
     const Tile &t = kTiles[i];
     const int64_t tiles = ((out_dim + t.bm - 1) / t.bm) * ((n_tok + t.bn - 1) / t.bn);
-    for (int splits = 1; splits <= kMaxSplit; splits *= 2) {
-      if (splits > 1 && (stages < 4 * splits || tiles * splits > t.slots || splits * out_bytes > (double)ws_bytes)) break;
-      const double groups = (double)tiles * splits;
+    // The kernels take whole pairs of stages, the largest tile whole groups of four.
+    const int64_t whole = i == 0 ? 4 : 2;
+    for (int want = 1; want <= kMaxSplit; want *= 2) {
+      const int64_t per_split = ((stages + want - 1) / want + whole - 1) / whole * whole;
+      const int64_t splits = (stages + per_split - 1) / per_split;
+      if (want > 1 && (stages < 4 * want || tiles * want > t.slots)) break;
+      if (splits > 1 && splits * out_bytes > (double)ws_bytes) break;
+      const double groups = (double)(tiles * splits);
       const double stage_us = groups <= 256 ? t.us_half : t.us_half + (t.us_full - t.us_half) * std::min(1.0, (groups - 256) / (t.slots - 256 + 1.0));
-      double us = std::max(1.0, groups / t.slots) * (double)stages / splits * stage_us;
+      double us = std::max(1.0, groups / t.slots) * (double)std::min(per_split, stages) * stage_us;
       if (splits > 1) us += kSplitUs + 2.0 * splits * out_bytes / kPartialBytesPerUs;
-      if ((i == 0 && splits == 1) || us < best_us) {
+      if ((i == 0 && want == 1) || us < best_us) {
         best_us = us;
-        best.tile = i;
-        best.splits = splits;
+        best = {i, (int)splits, (int)per_split};
       }
     }
   }
-  best.stages_per_split = (int)((stages + best.splits - 1) / best.splits + 1) / 2 * 2;  // taken in twos
-  best.splits = (int)((stages + best.stages_per_split - 1) / best.stages_per_split);
   return best;
 }
 

@@ -10,7 +10,8 @@
 // order, so that few rows still give the memory enough waves.  A compute unit takes
 // about 25 bytes a nanosecond from memory however many waves wait for them, so long
 // rows with too few of them for every unit are split between workgroups too (32768 ->
-// 1024 at one token 14.2 us with 64 workgroups, 8.7 with 256 and the join).
+// 1024 at one token 14.2 us with 64 workgroups, 8.7 with 256 and the join).  1024 ->
+// 32768 at one token: 5.5 us, 18 MB, of which 2 are the launch.
 #include <algorithm>
 #include <type_traits>
 

@@ -6,7 +6,9 @@
 // code stores are contiguous and the block maximum is two cross-lane moves.
 // The codes and scales of consecutive rows are contiguous whatever the row
 // stride of x, so the grid runs over groups of eight values of the whole
-// matrix; only the address of x needs the row.
+// matrix; only the address of x needs the row.  Measured, 2048 x 32768 bfloat16:
+// 36 us to quantize and 27 back, 170 MB each way (part of it still in the memory-side
+// cache), where a copy of that size takes 31; small matrices are the launch (2 us).
 #include "mxfp4_device.h"
 
 namespace mx {

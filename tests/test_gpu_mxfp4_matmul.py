@@ -175,3 +175,33 @@ def test_quantize_then_multiply():
     w, x = q8.mxfp4_quantize(wf), q8.mxfp4_quantize(xf)
     out = q8.mxfp4_matmul(w, x)
     _check(out, ref.values(*ref.quantize(ref.host(wf))), ref.values(*ref.quantize(ref.host(xf))))
+
+
+# Lengths that every tile shape splits into an even count of stages, into one that is
+# not a multiple of four, and unevenly; each regime's neighbours.
+@pytest.mark.parametrize("k,n,t", [
+    (17984, 1024, 4096), (17408, 7168, 512), (17696, 2048, 2048), (20000, 1000, 2500),
+    (9216, 512, 512), (5184, 640, 200), (7168, 2048, 129), (11296, 300, 700), (4128, 1024, 64), (33056, 96, 100),
+    (16416, 128, 33), (24640, 1024, 9), (40992, 256, 1), (2048, 8192, 32), (544, 64, 17), (512, 4096, 257),
+])
+def test_every_split_sums_every_value_once(k, n, t):
+    """Codes at scale 1 make products that are multiples of 1/4 and sums below 2^22:
+    every order of summation in fp32 is exact, and the result equals the 64-bit one."""
+    q8 = _q8()
+    g = torch.Generator(device="cuda").manual_seed(k + n + t)
+    w, x = (q8.Mxfp4(torch.randint(0, 256, (r, k // 2), dtype=torch.uint8, device="cuda", generator=g),
+                     torch.full((r, k // 32), 127, dtype=torch.uint8, device="cuda")) for r in (n, t))
+    assert k * 36 * 4 < 2 ** 24
+    want = q8.mxfp4_dequantize(x).double() @ q8.mxfp4_dequantize(w).double().t().contiguous()
+    assert torch.equal(q8.mxfp4_matmul(w, x).double(), want)
+
+
+@pytest.mark.parametrize("k,n,t", [(17984, 1024, 4096), (17408, 7168, 512), (8736, 512, 300), (40992, 256, 1), (5184, 640, 200)])
+def test_a_larger_workspace_changes_nothing(k, n, t):
+    q8 = _q8()
+    g = torch.Generator(device="cuda").manual_seed(k)
+    w, x = (q8.Mxfp4(torch.randint(0, 256, (r, k // 2), dtype=torch.uint8, device="cuda", generator=g),
+                     torch.randint(118, 122, (r, k // 32), dtype=torch.uint8, device="cuda", generator=g)) for r in (n, t))
+    need = q8.mxfp4_matmul_workspace_bytes(k, n, t)
+    more = torch.empty(4 * need + 256, dtype=torch.uint8, device="cuda")
+    assert torch.equal(q8.mxfp4_matmul(w, x), q8.mxfp4_matmul(w, x, workspace=more))
