@@ -11,8 +11,8 @@
 // (whose launch costs the caller 3 us more), 45.5 and 40.0 at 11.
 //
 // Measured, 4096 x 2048, 8 of 256 experts: one token 26.8 us (107 MB, 4.0 TB/s:
-// launches, routing and the tables' chain are 8 us of it), 64 tokens 527 us (3.0 GB
-// of 222 experts, 5.6 TB/s of the 5.9 that reading alone reaches).
+// launches, routing and the tables' chain are 8 us of it), 64 tokens 521 us (3.0 GB
+// of 222 experts, 5.7 TB/s of the 5.9 that reading alone reaches).
 //
 // A touched expert's tokens are the columns of 16x16x128 matrix instructions
 // (mxfp4_mfma.h), 16 of them a tile, so its weights are read once however many
@@ -250,13 +250,10 @@ __global__ __launch_bounds__(kThreads, SHORT ? 2 : 4) void up_kernel(const Args 
           const int64_t r = r0 + 16 * (q & 1);
           load_blocks<SHORT>((q < 2 ? a.gate : a.up) + r * (nb * 16), (q < 2 ? a.gate_s : a.up_s) + r * nb, off, nb, A[q]);
         }
-        __builtin_amdgcn_sched_barrier(0);  // all weights are on their way before any is used
-        if constexpr (EPL > 0) {
-          load_x(x_lds + tok * x_pitch(a.d_model), xs_lds + tok * x_scale_pitch(a.d_model), b0, nb, B);
-        } else {
-          load_blocks<SHORT>(a.tab.x, a.tab.x_s, Offsets4<SHORT>((uint32_t)tok, b0, nb), nb, B);
-          finish_blocks(off, B);
-        }
+        if constexpr (EPL == 0) load_blocks<SHORT>(a.tab.x, a.tab.x_s, Offsets4<SHORT>((uint32_t)tok, b0, nb), nb, B);
+        __builtin_amdgcn_sched_barrier(0);  // all of them are on their way before any is used
+        if constexpr (EPL > 0) load_x(x_lds + tok * x_pitch(a.d_model), xs_lds + tok * x_scale_pitch(a.d_model), b0, nb, B);
+        else finish_blocks(off, B);
 #pragma unroll
         for (int q = 0; q < 4; ++q) finish_blocks(off, A[q]);
 #pragma unroll
