@@ -1,0 +1,68 @@
+"""Matrices whose bytes, and outputs whose elements, do not fit 32-bit offsets.
+
+Codes at scale 1 give sums that fp32 holds exactly (products are multiples of
+1/4, at most 36 each), so equality does not depend on the order of summation."""
+import pytest
+import torch
+
+pytestmark = pytest.mark.gpu
+
+
+def _q8():
+    import q8_quantized_matmul_amd as q8
+    return q8
+
+
+def _mat(*shape, scale=127):
+    *lead, k = shape
+    return _q8().Mxfp4(torch.randint(0, 256, (*lead, k // 2), dtype=torch.uint8, device="cuda"),
+                       torch.full((*lead, k // 32), scale, dtype=torch.uint8, device="cuda"))
+
+
+def _rows(m, a, b):
+    return _q8().Mxfp4(m.codes[a:b].contiguous(), m.scales[a:b].contiguous())
+
+
+def _product(x, w):
+    q8 = _q8()
+    return q8.mxfp4_dequantize(x).double() @ q8.mxfp4_dequantize(w).double().t().contiguous()
+
+
+@pytest.mark.parametrize("t", [1, 24, 100])
+def test_weights_beyond_32_bits(t):
+    q8 = _q8()
+    n, k = 280000, 32768
+    assert n * k // 2 > 2 ** 32 and k * 36 * 4 < 2 ** 24
+    w, x = _mat(n, k), _mat(t, k)
+    out = q8.mxfp4_matmul(w, x)
+    for a in (0, 262140, n - 48):  # the first, those around byte 2^32, the last
+        assert torch.equal(out[:, a:a + 48].double(), _product(x, _rows(w, a, a + 48))), a
+
+
+@pytest.mark.parametrize("k,n,t", [(512, 32768, 70001), (32, 32768, 70001)])
+def test_output_beyond_32_bits(k, n, t):
+    q8 = _q8()
+    assert n * t > 2 ** 31
+    w, x = _mat(n, k), _mat(t, k)
+    out = q8.mxfp4_matmul(w, x)
+    for a in (0, 65520, t - 33):
+        assert torch.equal(out[a:a + 33].double(), _product(_rows(x, a, a + 33), w)), a
+
+
+@pytest.mark.parametrize("t", [1, 9])
+def test_experts_beyond_32_bits(t):
+    """Four experts at both ends of 300 give the same bits as a layer of those four."""
+    q8 = _q8()
+    e, d, f, ids = 300, 8192, 4096, [0, 260, 298, 299]
+    assert e * d * f // 2 > 2 ** 32
+    mats = [_mat(e, *shape, scale=116) for shape in ((f, d), (f, d), (d, f))]
+    x = torch.randn((t, d), device="cuda")
+    z = torch.full((t, e), -float("inf"), device="cuda")
+    few = torch.randn((t, 4), device="cuda")
+    z[:, ids] = few
+    out, sel, w = q8.mxfp4_moe_layer(x, z, *mats, 3)
+    small = [q8.Mxfp4(m.codes[ids].contiguous(), m.scales[ids].contiguous()) for m in mats]
+    out4, sel4, w4 = q8.mxfp4_moe_layer(x, few, *small, 3)
+    assert torch.isfinite(out).all() and out.abs().max() > 0
+    assert torch.equal(sel, torch.tensor(ids, dtype=torch.int32, device="cuda")[sel4.long()])
+    assert torch.equal(w, w4) and torch.equal(out, out4)
