@@ -58,7 +58,8 @@ class Mxfp4(NamedTuple):
 
 
 # A decode step makes these calls by the hundred: the raw forms of torch.cuda's
-# current device and stream cost a tenth of the public ones.
+# current device and stream cost a tenth of the public ones, and torch.empty takes
+# its sizes in 1.3 us one by one and in 1.7 as a tuple.
 _current_device = torch._C._cuda_getDevice
 _raw_stream = torch._C._cuda_getCurrentRawStream
 
@@ -133,14 +134,17 @@ def mxfp4_quantize(x: torch.Tensor, codes: torch.Tensor = None,
         raise ValueError("the values of a row of x must be adjacent")
     if k % MXFP4_BLOCK_ELEMS != 0:
         raise ValueError("k must be a multiple of 32")
+    given = codes is not None or scales is not None
     if codes is None:
-        codes = torch.empty((rows, k // 2), dtype=torch.uint8, device=device)
+        codes = torch.empty(rows, k // 2, dtype=torch.uint8, device=device)
     if scales is None:
-        scales = torch.empty((rows, k // MXFP4_BLOCK_ELEMS), dtype=torch.uint8, device=device)
+        scales = torch.empty(rows, k // MXFP4_BLOCK_ELEMS, dtype=torch.uint8, device=device)
     out = Mxfp4(codes, scales)
-    c, s, lead, k_out = _matrix(out, "out", device)
-    if k_out != k or lead.numel() != rows:
-        raise ValueError("codes and scales must hold as many rows and values as x")
+    if given:
+        _, _, lead, k_out = _matrix(out, "out", device)
+        if k_out != k or lead.numel() != rows:
+            raise ValueError("codes and scales must hold as many rows and values as x")
+    c, s = codes.data_ptr(), scales.data_ptr()
     _run("mxfp4_quantize", device, c, s, x.data_ptr(), _type(x.dtype, "x"), stride, rows, k)
     return out
 
@@ -151,7 +155,7 @@ def mxfp4_dequantize(m: Mxfp4, dtype: torch.dtype = torch.float32,
     device = _device(m[0], "codes")
     c, s, lead, k = _matrix(m, "m", device)
     if out is None:
-        out = torch.empty((*lead, k), dtype=dtype, device=device)
+        out = torch.empty(*lead, k, dtype=dtype, device=device)
         o = out.data_ptr()
     else:
         _shape(out, "out", *lead, k)
@@ -178,6 +182,7 @@ def _scratch(t, need: int, device):
         if need == 0:
             return None, 0, None
         t = torch.empty(need, dtype=torch.uint8, device=device)
+        return t.data_ptr(), need, t
     return _ptr(t, "workspace", torch.uint8, device), t.numel(), t
 
 
@@ -194,7 +199,7 @@ def mxfp4_matmul(w: Mxfp4, x: Mxfp4, out: torch.Tensor = None,
         raise ValueError("w must be [out_dim][k] and x [n_tok][k]")
     out_dim, n_tok = w_lead[0], x_lead[0]
     if out is None:
-        out = torch.empty((n_tok, out_dim), dtype=out_dtype, device=device)
+        out = torch.empty(n_tok, out_dim, dtype=out_dtype, device=device)
         o = out.data_ptr()
     else:
         _shape(out, "out", n_tok, out_dim)
@@ -210,15 +215,18 @@ def mxfp4_matmul(w: Mxfp4, x: Mxfp4, out: torch.Tensor = None,
 def _routing(selected, weights, n_tok: int, n_used: int, device):
     """(selected, its pointer, weights, its pointer), allocated where not given."""
     if selected is None:
-        selected = torch.empty((n_tok, n_used), dtype=torch.int32, device=device)
+        selected = torch.empty(n_tok, n_used, dtype=torch.int32, device=device)
+        sp = selected.data_ptr()
     else:
         _shape(selected, "selected", n_tok, n_used)
+        sp = _ptr(selected, "selected", torch.int32, device)
     if weights is None:
-        weights = torch.empty((n_tok, n_used), dtype=torch.float32, device=device)
+        weights = torch.empty(n_tok, n_used, dtype=torch.float32, device=device)
+        wp = weights.data_ptr()
     else:
         _shape(weights, "weights", n_tok, n_used)
-    return (selected, _ptr(selected, "selected", torch.int32, device),
-            weights, _ptr(weights, "weights", torch.float32, device))
+        wp = _ptr(weights, "weights", torch.float32, device)
+    return selected, sp, weights, wp
 
 
 def moe_topk(logits: torch.Tensor, n_used: int, bias: torch.Tensor = None,
@@ -280,7 +288,7 @@ def mxfp4_moe_layer(x: torch.Tensor, logits: torch.Tensor, gate: Mxfp4, up: Mxfp
         _shape(bias, "bias", n_expert)
         bias = _ptr(bias, "bias", torch.float32, device)
     if out is None:
-        out = torch.empty((n_tok, d_model), dtype=out_dtype or x.dtype, device=device)
+        out = torch.empty(n_tok, d_model, dtype=out_dtype or x.dtype, device=device)
     else:
         _shape(out, "out", n_tok, d_model)
     selected, sp, weights, wp = _routing(selected, weights, n_tok, n_used, device)
