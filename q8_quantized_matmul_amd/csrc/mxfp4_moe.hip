@@ -10,7 +10,7 @@
 // fused and with the front kernel: 31.2 and 32.2 us at 5 tokens, 39.3 and 38.0 at 8
 // (whose launch costs the caller 3 us more), 45.5 and 40.0 at 11.
 //
-// Measured, 4096 x 2048, 8 of 256 experts: one token 26.8 us (107 MB, 4.0 TB/s:
+// Measured, 4096 x 2048, 8 of 256 experts: one token 27.1 us (107 MB, 3.9 TB/s:
 // launches, routing and the tables' chain are 8 us of it), 64 tokens 521 us (3.0 GB
 // of 222 experts, 5.7 TB/s of the 5.9 that reading alone reaches).
 //

@@ -96,13 +96,14 @@ def _matrix(m, name: str, device):
     """(codes pointer, scales pointer, leading shape, k) of an MXFP4 matrix."""
     codes, scales = m
     cs, ss = codes.shape, scales.shape
-    if not cs or not ss or cs[-1] != 16 * ss[-1] or cs[:-1] != ss[:-1]:
+    lead = cs[:-1]
+    if not cs or not ss or cs[-1] != 16 * ss[-1] or lead != ss[:-1]:
         raise ValueError(f"{name}: codes {list(cs)} and scales {list(ss)} are not the two arrays of "
                          "one matrix ([..., k/2] and [..., k/32])")
     if not (codes.dtype == scales.dtype == torch.uint8 and codes.device == scales.device == device
             and codes.is_contiguous() and scales.is_contiguous()):
         raise ValueError(f"{name}: codes and scales must be contiguous uint8 on {device}")
-    return codes.data_ptr(), scales.data_ptr(), cs[:-1], 2 * cs[-1]
+    return codes.data_ptr(), scales.data_ptr(), lead, 2 * cs[-1]
 
 
 def _run(where: str, device, *args) -> None:
