@@ -159,8 +159,10 @@ size_t mxfp4_moe_layer_workspace_bytes(int64_t n_tok, int32_t n_used, int32_t n_
  *   gate  = W_gate[e_j] x4, up = W_up[e_j] x4          (products as mxfp4_matmul)
  *   mid   = silu(gate) * up, silu(g) = g / (1 + exp(-g)), after the optional
  *           limits (gate from above, up to +-clamp)    (fp32)
- *   out_t = sum_j w_j W_down[e_j] mxfp4_quantize(mid)  (fp32 sums, experts in a
- *           fixed order, rounded once)
+ *   out_t = sum_j w_j W_down[e_j] mxfp4_quantize(mid)  (fp32 sums, rounded once)
+ * Equal calls give equal bits.  The order in which a token's experts are summed
+ * depends on the sizes and on the experts that the call's tokens choose, so the
+ * last bits of a token alone and of the same token among others may differ.
  * Each touched expert's matrices are read once for all of its tokens.  Slots
  * without an eligible expert add nothing: a token whose logits are all
  * -infinity (padding) gives zeros.
