@@ -78,9 +78,9 @@ size_t mxfp4_matmul_workspace_bytes(int64_t in_dim, int64_t out_dim, int64_t n_t
  * output that uses it NaN.
  * n_tok == 0 or out_dim == 0 is a successful no-op.
  * Errors: in_dim % 32 != 0, in_dim == 0 with work to do, in_dim above 2^24,
- * out_dim or n_tok above 2^30, out_dim * n_tok above 2^38, negative sizes,
- * unknown type, null pointers -> Q8_0_EINVAL; codes or workspace not 16-byte aligned, out not aligned to its
- * type -> Q8_0_EALIGN. */
+ * out_dim or n_tok above 2^28, out_dim * n_tok above 2^35, negative sizes,
+ * unknown type, null pointers -> Q8_0_EINVAL; codes or workspace not 16-byte
+ * aligned, out not aligned to its type -> Q8_0_EALIGN. */
 int mxfp4_matmul(void *out, int32_t out_type, const void *w_codes, const void *w_scales,
                  int64_t in_dim, int64_t out_dim, const void *x_codes, const void *x_scales,
                  int64_t n_tok, void *workspace, size_t workspace_bytes, hipStream_t stream);
@@ -114,7 +114,7 @@ enum {
  * MOE_SOFTMAX compares z + bias in fp32; the other scores are formed and
  * compared in 64 bits.
  * Errors: n_expert outside [1, MOE_MAX_EXPERTS], n_used outside [1,
- * min(n_expert, MOE_MAX_USED)], n_tok * n_used above 2^31 - 1, unknown scoring,
+ * min(n_expert, MOE_MAX_USED)], n_tok above 2^25, unknown scoring,
  * null pointers -> Q8_0_EINVAL; pointers not 4-byte aligned -> Q8_0_EALIGN. */
 int moe_topk(int32_t *selected, float *weights, const float *logits, const float *bias,
              int64_t n_tok, int32_t n_expert, int32_t n_used, int32_t scoring,

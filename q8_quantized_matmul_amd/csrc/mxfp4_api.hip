@@ -24,8 +24,7 @@ bool type_ok(int32_t t) { return t == MXFP4_F32 || t == MXFP4_BF16 || t == MXFP4
 int type_size(int32_t t) { return t == MXFP4_F32 ? 4 : 2; }
 int status_of(hipError_t e) { return e == hipSuccess ? Q8_0_OK : Q8_0_ELAUNCH; }
 
-// A grid has fewer than 2^31 workgroups of 8192 values: the largest matrix the
-// elementwise kernels take.
+// The largest matrix of the elementwise kernels: 2^20 by 2^12 workgroups of 2048 values.
 constexpr int64_t kMaxElems = int64_t{1} << 43;
 
 // Sizes of a matrix that a call reads or writes: Q8_0_OK, or EINVAL.
@@ -35,8 +34,10 @@ int check_matrix(int64_t rows, int64_t k) {
   return Q8_0_OK;
 }
 
-// Sizes of a product: the kernels count blocks, rows, tokens and tiles in 32 bits.
-constexpr int64_t kMaxInDim = 1 << 24, kMaxRows = 1 << 30, kMaxOut = int64_t{1} << 38;
+// Sizes of a product: the kernels count blocks, rows, tokens and tiles in 32 bits, and a
+// launch has fewer than 2^32 threads: one for 16 outputs, and less than twice that where
+// the last row or token tile is cut.
+constexpr int64_t kMaxInDim = 1 << 24, kMaxRows = 1 << 28, kMaxOut = int64_t{1} << 35;
 int check_product(int64_t in_dim, int64_t out_dim, int64_t n_tok) {
   if (in_dim < 0 || out_dim < 0 || n_tok < 0 || in_dim % MXFP4_BLOCK_ELEMS != 0) return Q8_0_EINVAL;
   if (in_dim > kMaxInDim || out_dim > kMaxRows || n_tok > kMaxRows || out_dim * n_tok > kMaxOut)
@@ -54,12 +55,15 @@ bool use_gemm(int64_t in_dim, int64_t out_dim, int64_t n_tok) {
   return n_tok > 32 || in_dim <= 2048 || out_dim >= 8192;
 }
 
+// A wave each, and fewer than 2^32 threads a launch.
+constexpr int64_t kMaxRouteTokens = 1 << 25;
+
 int check_route(const float *logits, const float *bias, int64_t n_tok, int32_t n_expert,
                 int32_t n_used, int32_t scoring) {
   if (n_tok < 0 || n_expert < 1 || n_expert > MOE_MAX_EXPERTS || n_used < 1 || n_used > n_expert ||
       n_used > MOE_MAX_USED || scoring < MOE_SOFTMAX || scoring > MOE_SQRT_SOFTPLUS)
     return Q8_0_EINVAL;
-  if (n_tok > INT32_MAX / n_used) return Q8_0_EINVAL;
+  if (n_tok > kMaxRouteTokens) return Q8_0_EINVAL;
   if (n_tok == 0) return Q8_0_OK;
   if (!logits) return Q8_0_EINVAL;
   if (!aligned(logits, 4) || !aligned(bias, 4)) return Q8_0_EALIGN;

@@ -81,3 +81,21 @@ def test_experts_beyond_32_bits(t):
         y = torch.stack(alone, 1)  # [t][4][d]
         total = sum(w4[:, j, None].double() * y[torch.arange(t), sel4[:, j].long()] for j in range(3))
         assert ((out.double() - out4.double()).abs() <= 4.01 * 2.0 ** -24 * total).all()
+
+
+def test_quantizer_beyond_32_bits():
+    """More than 2^32 values, so more workgroups than the grid has along x: every slice
+    equals the slice's own result, and the bytes behind the end stay as they were."""
+    q8 = _q8()
+    rows, k = 131075, 32768
+    assert rows * k > 2 ** 32
+    x = torch.randn((rows, k), dtype=torch.bfloat16, device="cuda")
+    codes = torch.full((rows + 1, k // 2), 77, dtype=torch.uint8, device="cuda")
+    scales = torch.full((rows + 1, k // 32), 77, dtype=torch.uint8, device="cuda")
+    q8.mxfp4_quantize(x, codes=codes[:rows], scales=scales[:rows])
+    back = q8.mxfp4_dequantize(q8.Mxfp4(codes[:rows], scales[:rows]), torch.bfloat16)
+    for a in (0, 65534, 131070):  # the first, those around values 2^31 and 2^32
+        q = q8.mxfp4_quantize(x[a:a + 5])
+        assert torch.equal(codes[a:a + 5], q.codes) and torch.equal(scales[a:a + 5], q.scales), a
+        assert torch.equal(back[a:a + 5], q8.mxfp4_dequantize(q, torch.bfloat16)), a
+    assert (codes[rows] == 77).all() and (scales[rows] == 77).all()

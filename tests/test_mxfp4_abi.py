@@ -162,3 +162,21 @@ def test_valid_calls_without_device_report_nodev(q8, lib):
     assert lib.mxfp4_dequantize(FAKE, 0, FAKE, FAKE, 2, 64, None) == q8.Q8_0_ENODEV
     assert lib.moe_topk(FAKE, FAKE, FAKE, None, 4, 256, 8, 0, 1, 1.0, None) == q8.Q8_0_ENODEV
     assert lib.mxfp4_matmul(FAKE, 0, FAKE, FAKE, 64, 16, FAKE, FAKE, 2, None, 0, None) == q8.Q8_0_ENODEV
+
+
+def test_sizes_at_the_limits(q8, lib):
+    """The largest sizes pass the checks (and find no device), one more does not."""
+    if torch.cuda.device_count() > 0:
+        pytest.skip("a device is present")
+
+    def mm(k, n, t):
+        return lib.mxfp4_matmul(FAKE, 1, FAKE, FAKE, k, n, FAKE, FAKE, t, None, 0, None)
+    assert mm(1 << 24, 1 << 28, 128) == mm(32, 128, 1 << 28) == q8.Q8_0_ENODEV
+    assert mm((1 << 24) + 32, 1, 1) == mm(32, (1 << 28) + 1, 1) == mm(32, 1, (1 << 28) + 1) == q8.Q8_0_EINVAL
+    assert mm(32, 1 << 28, 129) == q8.Q8_0_EINVAL
+
+    def topk(t):
+        return lib.moe_topk(FAKE, FAKE, FAKE, None, t, 8, 2, 0, 1, 1.0, None)
+    assert topk(1 << 25) == q8.Q8_0_ENODEV and topk((1 << 25) + 1) == q8.Q8_0_EINVAL
+    assert lib.mxfp4_quantize(FAKE, FAKE, FAKE, 1, 1 << 20, 1 << 23, 1 << 20, None) == q8.Q8_0_ENODEV
+    assert lib.mxfp4_quantize(FAKE, FAKE, FAKE, 1, 1 << 20, (1 << 23) + 1, 1 << 20, None) == q8.Q8_0_EINVAL
