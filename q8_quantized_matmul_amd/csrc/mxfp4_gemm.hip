@@ -10,8 +10,8 @@
 // What bounds it: 256 workgroups of 256^2 tiles take 1.55 us a stage, of which the
 // copies alone are 1.3 (the second caches' rate) and the matrix instructions alone
 // 1.34 (6.4 PFLOP/s, what the chip holds on random values for its power; 9.6 on
-// constant ones); then the stores and the join of the splits.  8192^3 311 us, 3.5
-// PFLOP/s; 32768 -> 1024 at 2048 tokens 48 us and 7 for the join; 4096 -> 2048 at
+// constant ones); then the stores and the join of the splits.  8192^3 306 us, 3.6
+// PFLOP/s; 32768 -> 1024 at 2048 tokens 46 us and 7 for the join; 4096 -> 2048 at
 // 200 9.2 us, two thirds of it launch, first loads and stores.
 //
 // LDS: 128 bytes a row; the 16-byte block c of row r lies at position c ^ (r / 2 % 8),
@@ -109,7 +109,7 @@ __device__ __forceinline__ void tile_of(const GemmArgs &a, int &tn, int &tt, int
 }
 
 template <int WM, int WN, int TM, int TN, int RING, int TYPE>
-__global__ __launch_bounds__(64 * WM * WN, WM * WN / 4) void gemm_kernel(const GemmArgs a) {
+__global__ __launch_bounds__(64 * WM * WN, 2) void gemm_kernel(const GemmArgs a) {
   constexpr int kW = WM * WN, kThreads = 64 * kW;
   constexpr int BM = 32 * TM * WM, BN = 32 * TN * WN, ROWS = BM + BN;
   constexpr int COPIES = ROWS / 8 / kW;  // copy instructions of a wave per stage
@@ -357,24 +357,36 @@ __global__ __launch_bounds__(64 * WM * WN, WM * WN / 4) void gemm_kernel(const G
     stage(st, s0);
     stage(st + 1, s1);
   }
-  wait_memory<0>();  // no copy outlives the workgroup
+  wait_memory<0>();
+  __builtin_amdgcn_s_barrier();  // every wave's copies have landed, and been read
 
+  // Through LDS, a region a wave, so that a store writes whole lines of out: as the
+  // lanes hold them it would write 32 bytes of 32 rows (1024 -> 32768 at 512 tokens 26.0
+  // us, so 22.4; 4096^3 50 and 48).  The 16-byte chunk c of row r
+  // lies at c ^ (r % 16) (% 8 in rows of eight), which spreads rows over the banks.
+  constexpr int kChunks = TM * 8, kSwizzle = (kChunks < 16 ? kChunks : 16) - 1;
+  static_assert(kW * 32 * kChunks * 16 <= RING * ROWS * kRowBytes, "the regions fit in the stages' places");
+  uint8_t *mine = &lds[0][0] + wave * (32 * kChunks * 16);
   const int64_t base = (int64_t)ts * a.t * a.n;
 #pragma unroll
   for (int j = 0; j < TN; ++j) {
-    const int t = t0 + 32 * (wn * TN + j) + lrow;
 #pragma unroll
-    for (int i = 0; i < TM; ++i) {
-      __builtin_amdgcn_sched_barrier(0);
+    for (int i = 0; i < TM; ++i)
 #pragma unroll
-      for (int q = 0; q < 4; ++q) {
-        const int o = n0 + 32 * (wm * TM + i) + 8 * q + 4 * h;
-        if (t < a.t && o < a.n) {
-          const f32x4 v = {acc[i][j][4 * q], acc[i][j][4 * q + 1], acc[i][j][4 * q + 2], acc[i][j][4 * q + 3]};
-          store4<TYPE>(a.out, base + (int64_t)t * a.n + o, v, a.n - o, a.wide);
-        }
-      }
+      for (int q = 0; q < 4; ++q)
+        *reinterpret_cast<f32x4 *>(mine + (lrow * kChunks + ((8 * i + 2 * q + h) ^ (lrow & kSwizzle))) * 16) =
+            f32x4{acc[i][j][4 * q], acc[i][j][4 * q + 1], acc[i][j][4 * q + 2], acc[i][j][4 * q + 3]};
+    __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+    __builtin_amdgcn_wave_barrier();
+#pragma unroll
+    for (int k = 0; k < 32 * kChunks / 64; ++k) {
+      const int at = k * 64 + lane, r = at / kChunks, c = at % kChunks;
+      const f32x4 v = *reinterpret_cast<const f32x4 *>(mine + (r * kChunks + (c ^ (r & kSwizzle))) * 16);
+      const int t = t0 + 32 * (wn * TN + j) + r, o = n0 + 32 * wm * TM + 4 * c;
+      if (t < a.t && o < a.n) store4<TYPE>(a.out, base + (int64_t)t * a.n + o, v, a.n - o, a.wide);
     }
+    __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+    __builtin_amdgcn_wave_barrier();
   }
 }
 
