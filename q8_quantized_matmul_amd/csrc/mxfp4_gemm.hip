@@ -295,7 +295,11 @@ __global__ __launch_bounds__(64 * WM * WN, 2) void gemm_kernel(const GemmArgs a)
     read_stage((buf + 1) % RING, next);
     if constexpr (U == 3) read_scales();
     copy(min(st + RING, last), buf);
-    if constexpr (U == 0) fetch_scales(st + 4);
+    if constexpr (U == 0) {
+      // Behind the copies: the waits of the next stages leave room for it, and not for them.
+      __builtin_amdgcn_sched_barrier(0);
+      fetch_scales(st + 4);
+    }
     __builtin_amdgcn_sched_barrier(0);
     multiply(s0, u_c, now);
     multiply(s1, u_c, now);
