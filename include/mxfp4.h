@@ -74,8 +74,11 @@ size_t mxfp4_matmul_workspace_bytes(int64_t in_dim, int64_t out_dim, int64_t n_t
  *            NULL / 0 is always valid.  Calls that share a workspace must not
  *            overlap in time.
  * Products are exact and summed in fp32: |out - exact| <= (in_dim / 32 + 8) *
- * 2^-23 * sum |w x| before the rounding to out_type.  A NaN block makes every
- * output that uses it NaN.
+ * 2^-23 * sum |w x| + in_dim * 2^-125 before the rounding to out_type (the second
+ * part is what terms and sums below fp32's normal numbers may lose).  Where a term
+ * or a partial sum exceeds fp32's largest number, as it can where sum |w x| reaches
+ * 2^127, that output is infinite or NaN; no other output is touched.  A NaN block
+ * makes every output that uses it NaN.
  * n_tok == 0 or out_dim == 0 is a successful no-op.
  * Errors: in_dim % 32 != 0, in_dim == 0 with work to do, in_dim above 2^24,
  * out_dim or n_tok above 2^28, out_dim * n_tok above 2^35, negative sizes,
