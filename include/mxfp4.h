@@ -53,8 +53,10 @@ int mxfp4_quantize(void *codes, void *scales, const void *x, int32_t x_type, int
 
 /* The values an MXFP4 matrix stands for.
  *   out : [n_rows][in_dim] of out_type, row-major, written.  Exact in fp32 and bf16
- *         for every block (subnormals included); fp16 rounds to nearest even and
- *         overflows to infinity.  Blocks of scale byte 255 give NaN.
+ *         (subnormals included) but for values of 2^128 and above, which scale bytes
+ *         253 and 254 can stand for and mxfp4_quantize does not make (252 is its
+ *         largest): those are infinite.  fp16 rounds to nearest even and overflows to
+ *         infinity.  Blocks of scale byte 255 give NaN.
  * Errors as mxfp4_quantize (out needs 16-byte alignment). */
 int mxfp4_dequantize(void *out, int32_t out_type, const void *codes, const void *scales,
                      int64_t n_rows, int64_t in_dim, hipStream_t stream);

@@ -152,7 +152,8 @@ def mxfp4_quantize(x: torch.Tensor, codes: torch.Tensor = None,
 
 def mxfp4_dequantize(m: Mxfp4, dtype: torch.dtype = torch.float32,
                      out: torch.Tensor = None) -> torch.Tensor:
-    """The values [..., k] that an MXFP4 matrix stands for (exact in float32 and bfloat16)."""
+    """The values [..., k] that an MXFP4 matrix stands for: exact in float32 and bfloat16
+    but for values of 2^128 and above (scale bytes 253 and 254), which are infinite."""
     device = _device(m[0], "codes")
     c, s, lead, k = _matrix(m, "m", device)
     if out is None:

@@ -1,4 +1,4 @@
-"""GPU tests of mxfp4_matmul at both ends of the scale range, against 64 bits.
+"""GPU tests of mxfp4_matmul, and of mxfp4_dequantize, at both ends of the scale range, against 64 bits.
 
 A block's values reach from 2^-128 to 6 * 2^127, so the terms of a product leave
 fp32's normal numbers on both sides.  Below 2^-126 a term, or one of the at most
@@ -59,3 +59,21 @@ def test_terms_above_the_largest_number(k, n, t):
     assert finite[small].all() and not finite[large].any()
     assert (np.abs(got - want) <= _bound(k, mag))[finite].all()
     assert np.isposinf(got[-1, n - 1])
+
+
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
+def test_the_largest_scales_dequantized(dtype):
+    """Exact below 2^128 and infinite from there on; what the quantizer makes of the
+    largest numbers is below."""
+    import q8_quantized_matmul_amd as q8
+    codes = np.tile(np.arange(256, dtype=np.uint8).reshape(16, 16), (3, 1))
+    scales = np.repeat(np.array([252, 253, 254], dtype=np.uint8), 16)[:, None]
+    got, want = ref.host(q8.mxfp4_dequantize(ref.device(q8, (codes, scales)), dtype)), ref.values(codes, scales)
+    large = np.abs(want) >= 2.0 ** 128
+    assert large[16:].any() and not large[:16].any()
+    assert np.array_equal(got, np.where(large, np.copysign(np.inf, want), want))
+    x = torch.full((2, 64), torch.finfo(dtype).max, dtype=dtype, device="cuda")
+    x[1] = -x[1]
+    q = q8.mxfp4_quantize(x)
+    assert (q.scales == 252).all()
+    assert torch.equal(q8.mxfp4_dequantize(q, dtype), torch.sign(x) * 6 * 2.0 ** 125)
