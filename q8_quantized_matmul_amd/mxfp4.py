@@ -18,6 +18,7 @@ from . import Q8Error, _i32, _i64, _lib, _sz, _vp
 MXFP4_BLOCK_ELEMS = 32
 MXFP4_F32, MXFP4_BF16, MXFP4_F16 = 0, 1, 2
 MOE_SOFTMAX, MOE_SIGMOID, MOE_SQRT_SOFTPLUS = 0, 1, 2
+_I32_MAX = 2 ** 31 - 1
 _TYPES = {torch.float32: MXFP4_F32, torch.bfloat16: MXFP4_BF16, torch.float16: MXFP4_F16}
 
 class MoeLayerArgs(ctypes.Structure):
@@ -90,6 +91,12 @@ def _device(t: torch.Tensor, name: str) -> torch.device:
 def _shape(t: torch.Tensor, name: str, *shape) -> None:
     if t.shape != shape:
         raise ValueError(f"{name} must have shape {list(shape)}, got {list(t.shape)}")
+
+
+def _route_sizes(n_expert: int, n_used: int, scoring: int) -> None:
+    """Refuses what the C call's 32-bit arguments would take for another number."""
+    if n_expert > _I32_MAX or n_used > _I32_MAX or scoring > _I32_MAX:
+        raise ValueError("n_expert, n_used and scoring must be below 2^31")
 
 
 def _matrix(m, name: str, device):
@@ -241,6 +248,7 @@ def moe_topk(logits: torch.Tensor, n_used: int, bias: torch.Tensor = None,
         raise ValueError("logits must be [n_tok][n_expert]")
     device = _device(logits, "logits")
     n_tok, n_expert = logits.shape
+    _route_sizes(n_expert, n_used, scoring)
     selected, sp, weights, wp = _routing(selected, weights, n_tok, n_used, device)
     if bias is not None:
         _shape(bias, "bias", n_expert)
@@ -252,6 +260,7 @@ def moe_topk(logits: torch.Tensor, n_used: int, bias: torch.Tensor = None,
 
 def mxfp4_moe_layer_workspace_bytes(n_tok: int, n_used: int, n_expert: int, d_model: int,
                                     d_ff: int) -> int:
+    _route_sizes(n_expert, n_used, 0)
     return int(_lib.mxfp4_moe_layer_workspace_bytes(n_tok, n_used, n_expert, d_model, d_ff))
 
 
@@ -278,6 +287,7 @@ def mxfp4_moe_layer(x: torch.Tensor, logits: torch.Tensor, gate: Mxfp4, up: Mxfp
         raise ValueError("x must be [n_tok][d_model] and logits [n_tok][n_expert]")
     n_tok, d_model = x.shape
     n_expert = logits.shape[1]
+    _route_sizes(n_expert, n_used, scoring)
     gc, gs, g_lead, gk = _matrix(gate, "gate", device)
     uc, us, u_lead, uk = _matrix(up, "up", device)
     dc, ds, d_lead, d_ff = _matrix(down, "down", device)
