@@ -92,7 +92,7 @@ int mxfp4_matmul(void *out, int32_t out_type, const void *w_codes, const void *w
 
 /* Scores of moe_topk, from a token's logits z. */
 enum {
-    MOE_SOFTMAX = 0,      /* exp(z) / sum exp(z); ordered by z itself */
+    MOE_SOFTMAX = 0,      /* exp(z) / sum exp(z); ordered by z + bias */
     MOE_SIGMOID = 1,      /* 1 / (1 + exp(-z))                       */
     MOE_SQRT_SOFTPLUS = 2 /* sqrt(log(1 + exp(z)))                   */
 };
@@ -100,22 +100,27 @@ enum {
 #define MOE_MAX_EXPERTS 1024
 #define MOE_MAX_USED 32
 
-/* The router: each token's n_used experts of largest score + bias, largest
- * first, ties to the lowest id, with their weights.  Its outputs are the
- * `selected` and `weights` of q8_0_moe_ffn and q8_0_moe_grouped.
+/* The router: each token's n_used experts of largest key, largest first, ties to
+ * the lowest id, with their weights.  Its outputs are the `selected` and `weights`
+ * of q8_0_moe_ffn and q8_0_moe_grouped.
+ *   key      : score + bias for MOE_SIGMOID and MOE_SQRT_SOFTPLUS; the logit + bias
+ *              for MOE_SOFTMAX.  Without a bias that is the order of the
+ *              probabilities, with one the order of probability * exp(bias).  A
+ *              bias that a model adds to the softmax probabilities themselves gives
+ *              another order and is not what this call computes.
  *   selected : int32 [n_tok][n_used], written.
- *   weights  : fp32 [n_tok][n_used], written: the scores (without bias) of the
- *              chosen experts, divided by their sum if renormalize is set (for
- *              MOE_SOFTMAX without it, by the sum over all experts), times `scale`
- *              (a sum of exactly zero divides nothing: those weights are 0).
+ *   weights  : fp32 [n_tok][n_used], written: the scores (without bias, rounded to
+ *              fp32) of the chosen experts, divided by their sum if renormalize is
+ *              set (for MOE_SOFTMAX without it, by the sum over all experts), times
+ *              `scale` (a sum of exactly zero divides nothing: those weights are 0).
  *   logits   : fp32 [n_tok][n_expert] (a router projection's output).
- *   bias     : fp32 [n_expert] added to the score for the choice only (to the
- *              logit for MOE_SOFTMAX), or NULL.
- * An expert whose logit or biased score is -infinity is never chosen: a token
- * with fewer than n_used others gets id -1 and weight 0 in its last slots (all
- * of them for a token whose logits are all -infinity, e.g. padding).  NaN keys
- * come before all others, and a NaN or +infinite score among those summed
- * makes the weights that its sum divides NaN.
+ *   bias     : fp32 [n_expert], part of the key only, or NULL.
+ * An expert whose logit or key is -infinity is never chosen: a token with fewer
+ * than n_used others gets id -1 and weight 0 in its last slots (all of them for a
+ * token whose logits are all -infinity, e.g. padding).  NaN keys come before all
+ * others.  A NaN score among those summed makes the weights that its sum divides
+ * NaN, and so does a +infinite logit for MOE_SOFTMAX; a +infinite MOE_SQRT_SOFTPLUS
+ * score that is divided by its sum is NaN itself, beside others of 0.
  * MOE_SOFTMAX compares z + bias in fp32; the other scores are formed and
  * compared in 64 bits.
  * Errors: n_expert outside [1, MOE_MAX_EXPERTS], n_used outside [1,

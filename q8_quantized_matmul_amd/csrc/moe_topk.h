@@ -1,10 +1,10 @@
 // moe_topk.h -- the MoE router's top-k of one token, on one wave.
 //
-// Lane l holds experts l, l + 64, ... .  An expert's key (its score plus bias)
-// becomes an unsigned number of the same order, 0 meaning "not eligible".  Softmax
-// keys order by the logits themselves, in 32 bits; sigmoid and sqrt(softplus) keys
-// are compared in 64 bits, where neither rounding nor the math functions' last
-// bits move an expert across another.
+// Lane l holds experts l, l + 64, ... .  An expert's key becomes an unsigned number
+// of the same order, 0 meaning "not eligible".  Softmax keys are logit plus bias, in
+// 32 bits; sigmoid and sqrt(softplus) keys are score plus bias and compared in 64
+// bits, where neither rounding nor the math functions' last bits move an expert
+// across another.
 //
 // The n_used-th largest of the lanes' maxima is no more than the n_used-th largest
 // key, so the keys from it up hold all that are chosen, and mostly few others.

@@ -242,8 +242,9 @@ def moe_topk(logits: torch.Tensor, n_used: int, bias: torch.Tensor = None,
              scoring: int = MOE_SOFTMAX, renormalize: bool = True, scale: float = 1.0,
              selected: torch.Tensor = None, weights: torch.Tensor = None):
     """(selected int32, weights float32), both [n_tok][n_used]: each token's experts of
-    largest score + bias from float32 logits [n_tok][n_expert].  Slots without an
-    eligible expert (logits of -inf) hold id -1 and weight 0."""
+    largest score + bias from float32 logits [n_tok][n_expert]; for MOE_SOFTMAX of
+    largest logit + bias, which a bias on the probabilities does not equal.  Slots
+    without an eligible expert (logits of -inf) hold id -1 and weight 0."""
     if logits.dim() != 2:
         raise ValueError("logits must be [n_tok][n_expert]")
     device = _device(logits, "logits")
