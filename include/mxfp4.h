@@ -173,9 +173,10 @@ size_t mxfp4_moe_layer_workspace_bytes(int64_t n_tok, int32_t n_used, int32_t n_
  * Equal calls give equal bits.  The order in which a token's experts are summed
  * depends on the sizes and on the experts that the call's tokens choose, so the
  * last bits of a token alone and of the same token among others may differ.
- * Each touched expert's matrices are read once for all of its tokens.  Slots
- * without an eligible expert add nothing: a token whose logits are all
- * -infinity (padding) gives zeros.
+ * Each touched expert's matrices are loaded once for every 16 of its tokens, and
+ * the activation is the plain SwiGLU above, without biases.  Slots without an
+ * eligible expert add nothing: a token whose logits are all -infinity (padding)
+ * gives zeros.
  *   workspace : device memory, 256-byte aligned, contents on entry do not
  *     matter; calls that share one must not overlap in time.
  * Errors: bad sizes (as above and moe_topk's; d_model and d_ff up to 2^20;

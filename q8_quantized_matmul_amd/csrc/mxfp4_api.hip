@@ -47,9 +47,9 @@ int check_product(int64_t in_dim, int64_t out_dim, int64_t n_tok) {
 
 // The tiled kernel above 32 tokens; from 17 on where its stages are few or its rows
 // many; and never for rows of less than 512 values, whose scales it cannot fetch.
-// Measured (us, streaming / tiled): 4096 -> 2048 at 16 tokens 4.9 / 7.0, at 32 6.2 /
-// 7.0, at 64 8.5 / 6.8; 1024 -> 4096 at 32 6.1 / 4.2; 1024 -> 32768 at 32 10.1 / 7.3;
-// 32768 -> 1024 at 32 12.8 / 13.8, at 64 17.8 / 14.2.
+// Measured (us, streaming / tiled): 4096 -> 2048 at 16 tokens 5.0 / 7.7, at 32 6.3 /
+// 8.0, at 64 8.6 / 6.8; 1024 -> 4096 at 32 6.2 / 4.2; 1024 -> 32768 at 32 10.3 / 7.5;
+// 32768 -> 1024 at 32 12.9 / 13.9, at 64 17.8 / 14.4.
 bool use_gemm(int64_t in_dim, int64_t out_dim, int64_t n_tok) {
   if (in_dim < 512 || n_tok <= 16) return false;
   return n_tok > 32 || in_dim <= 2048 || out_dim >= 8192;

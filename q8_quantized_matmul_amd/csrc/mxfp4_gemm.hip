@@ -4,15 +4,24 @@
 // A workgroup of WM x WN waves computes 32 TM WM weight rows x 32 TN WN tokens.
 // A stage is 256 values of every row, one 128-byte line: the copies go straight
 // from memory to LDS, 1 KB (eight rows) an instruction, into the RING places that
-// stages take in turn, so the copies of the next ones are in flight while one is
-// multiplied, with one barrier a stage.
+// stages take in turn, with one barrier a stage; while one stage is multiplied the
+// copies of a later one are in flight.
+//
+// They are so for one stage at most, whatever RING is.  The waits written here are
+// counted, but the compiler, to which every place is the same array, adds waits for all
+// copies in flight: in the 64x64 kernel in front of each stage's LDS reads (so its ring
+// of four runs as one of two), in the 256x256 kernel at the start of three stages in
+// four, right behind the issue of their successors' copies.  In the other two no copies
+// are in flight where it would.
 //
 // What bounds it: 256 workgroups of 256^2 tiles take 1.55 us a stage, of which the
 // copies alone are 1.3 (the second caches' rate) and the matrix instructions alone
 // 1.34 (6.4 PFLOP/s, what the chip holds on random values for its power; 9.6 on
-// constant ones); then the stores and the join of the splits.  8192^3 306 us, 3.6
-// PFLOP/s; 32768 -> 1024 at 2048 tokens 46 us and 7 for the join; 4096 -> 2048 at
-// 200 9.2 us, two thirds of it launch, first loads and stores.
+// constant ones); then the waits above, the stores and the join of the splits.  8192^3
+// 306 us, 3.6 PFLOP/s (bf16 outputs 283 to 290); 4096^3 47 (43); 32768 -> 1024 at 2048
+// tokens 46 us and 7 for the join; 4096 -> 2048 at 200 7.2 us with two sets of weights in
+// turn, 9.1 with four: launch, first loads, sixteen stages of 0.4 us, which is the
+// latency of their copies behind four matrix instructions, and stores.
 //
 // LDS: 128 bytes a row; the 16-byte block c of row r lies at position c ^ (r / 2 % 8),
 // which the copies get by reading that block from memory (a lane's place in LDS
@@ -287,8 +296,8 @@ __global__ __launch_bounds__(64 * WM * WN, 2) void gemm_kernel(const GemmArgs a)
     constexpr int U = decltype(u_c)::value, buf = U % RING;
     constexpr std::integral_constant<int, U & 1> now{};
     constexpr std::integral_constant<int, (U & 1) ^ 1> next{};
-    // The stage is in registers and the next one's copies have landed; later copies and
-    // a scale fetch may be outstanding.
+    // The stage is in registers and the next one's copies have landed; of the counted
+    // operations later copies and a scale fetch may be outstanding.
     wait_memory<(RING - 2) * COPIES + (U >= 1 && U < RING ? FETCHES : 0)>();
     __builtin_amdgcn_s_barrier();
     __builtin_amdgcn_sched_barrier(0);
@@ -365,8 +374,9 @@ __global__ __launch_bounds__(64 * WM * WN, 2) void gemm_kernel(const GemmArgs a)
   __builtin_amdgcn_s_barrier();  // every wave's copies have landed, and been read
 
   // Through LDS, a region a wave, so that a store writes whole lines of out: as the
-  // lanes hold them it would write 32 bytes of 32 rows (1024 -> 32768 at 512 tokens 26.0
-  // us, so 22.4; 4096^3 50 and 48).  The 16-byte chunk c of row r
+  // lanes hold them it would write 32 bytes of 32 rows (1024 -> 32768 at 512 tokens 26.9
+  // us, so 22.8, with bf16 outputs 24.3 and 20.1; 4096^3 49 and 47, 49 and 43; 8192^3
+  // 311 and 306, 304 and 290).  The 16-byte chunk c of row r
   // lies at c ^ (r % 16) (% 8 in rows of eight), which spreads rows over the banks.
   constexpr int kChunks = TM * 8, kSwizzle = (kChunks < 16 ? kChunks : 16) - 1;
   static_assert(kW * 32 * kChunks * 16 <= RING * ROWS * kRowBytes, "the regions fit in the stages' places");
@@ -433,11 +443,11 @@ constexpr float kSplitUs = 4.0f, kPartialBytesPerUs = 4.0e6f;
 
 // The tile and split of the smallest estimated time.  Large tiles read each row
 // fewer times, small ones give every compute unit work, and a split over K does
-// for long rows what small tiles do for many.  Measured, microseconds, chosen
-// first: 4096 -> 4096 at 4096 tokens 256^2 tiles 46, 128^2 54; 4096 -> 2048 at 4096
-// 128^2 28, 256^2 40; at 2048 128x64 20, 64^2 23; at 1024 64^2 13.1, 128x64 15.1;
-// 32768 -> 1024 at 2048 128^2 in 4 splits 53, 256^2 in 8 63, 128x64 in 2 61; 7168 ->
-// 2048 at 129 64^2 in 2 splits 11.4, unsplit 13.2.
+// for long rows what small tiles do for many.  Measured, microseconds, fp32 outputs,
+// chosen first: 4096 -> 4096 at 4096 tokens 256^2 tiles 47, 128^2 52; 4096 -> 2048 at
+// 4096 128^2 28, 256^2 35; at 2048 128x64 18.9, 64^2 22.0; at 1024 64^2 12.4, 128x64
+// 14.3; 32768 -> 1024 at 2048 128^2 in 4 splits 54, 256^2 in 8 59, 128x64 in 2 59; 7168
+// -> 2048 at 129 64^2 in 2 splits 11.5, unsplit 13.2.
 GemmPlan gemm_plan(int64_t in_dim, int64_t out_dim, int64_t n_tok, size_t ws_bytes) {
   const int64_t stages = (in_dim / kBlock + kStageBlocks - 1) / kStageBlocks;
   const double out_bytes = 4.0 * (double)out_dim * (double)n_tok;
