@@ -109,10 +109,11 @@ enum {
  *              bias that a model adds to the softmax probabilities themselves gives
  *              another order and is not what this call computes.
  *   selected : int32 [n_tok][n_used], written.
- *   weights  : fp32 [n_tok][n_used], written: the scores (without bias, rounded to
- *              fp32) of the chosen experts, divided by their sum if renormalize is
- *              set (for MOE_SOFTMAX without it, by the sum over all experts), times
- *              `scale` (a sum of exactly zero divides nothing: those weights are 0).
+ *   weights  : fp32 [n_tok][n_used], written: the scores (without bias) of the
+ *              chosen experts, divided by their sum if renormalize is set (for
+ *              MOE_SOFTMAX without it, by the sum over all experts), times `scale`.
+ *              The sum may lie far below fp32's range; where it is zero in 64 bits
+ *              (logits below -745) it divides nothing and those weights are 0.
  *   logits   : fp32 [n_tok][n_expert] (a router projection's output).
  *   bias     : fp32 [n_expert], part of the key only, or NULL.
  * An expert whose logit or key is -infinity is never chosen: a token with fewer

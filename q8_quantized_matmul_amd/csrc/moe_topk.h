@@ -96,6 +96,14 @@ __device__ __forceinline__ float permute(int to, float v) {
   return __builtin_bit_cast(float, permute(to, __builtin_bit_cast(int, v)));
 }
 
+// A score on its way from its expert's lane to its slot: the bits of a double, or, for
+// softmax, of the fp32 logit in the high half alone.
+typedef uint64_t Score;
+__device__ __forceinline__ Score pack(double s) { return __builtin_bit_cast(uint64_t, s); }
+__device__ __forceinline__ Score pack(float z) { return (uint64_t)__builtin_bit_cast(uint32_t, z) << 32; }
+__device__ __forceinline__ double score_of(Score s) { return __builtin_bit_cast(double, s); }
+__device__ __forceinline__ float logit_of(Score s) { return __builtin_bit_cast(float, high(s)); }
+
 // A number that at least n_used of the lanes' keys (or all that are not 0) reach.
 __device__ __forceinline__ uint32_t border_of(uint32_t best, int n_used) {
   uint32_t top = 0;
@@ -108,11 +116,11 @@ __device__ __forceinline__ uint32_t border_of(uint32_t best, int n_used) {
   return top;
 }
 
-// Slots of the candidates, lanes `who` with a key, an expert and its score each; of
-// equal keys the lower lane is first.
+// Slots of the candidates, lanes `who` with a key, an expert and its score (softmax: its
+// logit) each; of equal keys the lower lane is first.
 template <typename K>
-__device__ __forceinline__ void place(uint64_t who, K key, int expert, float score, int n_used, int lane,
-                                      int &id, float &sc) {
+__device__ __forceinline__ void place(uint64_t who, K key, int expert, Score score, bool softmax, int n_used,
+                                      int lane, int &id, Score &sc) {
   int before = 0;
   for (uint64_t left = who; left != 0; left &= left - 1) {
     const int c = __ffsll((unsigned long long)left) - 1;
@@ -123,9 +131,10 @@ __device__ __forceinline__ void place(uint64_t who, K key, int expert, float sco
   // nobody sends to get zeros.
   const int to = ((who >> lane) & 1) && before < n_used ? before : 63;
   id = permute(to, expert + 1) - 1;
-  sc = permute(to, score);
+  sc = (uint64_t)(uint32_t)permute(to, (int)high(score)) << 32;
+  if (!softmax) sc |= (uint32_t)permute(to, (int)(uint32_t)score);
   if (lane >= n_used) id = -1;
-  if (id < 0) sc = 0.0f;
+  if (id < 0) sc = 0;
 }
 
 // The candidates among EPL experts a lane, those with keys (or upper bounds of
@@ -160,26 +169,26 @@ __device__ __forceinline__ int gather(const uint32_t (&key)[EPL], uint32_t borde
   return total;
 }
 
-// An expert's key in 64 bits (0: not eligible), and its score.
-__device__ __forceinline__ uint64_t key_of(const RouteArgs &a, float z, float b, float &score) {
-  score = z;
+// An expert's key in 64 bits (0: not eligible), and its score (for softmax its logit).
+__device__ __forceinline__ uint64_t key_of(const RouteArgs &a, float z, float b, Score &score) {
+  score = pack(z);
   if (z == -__builtin_huge_valf()) return 0;
   if (a.scoring == kSoftmax) return (uint64_t)order32(z + b + 0.0f) << 32;
   const double s = score64(a.scoring, z);
-  score = (float)s;
+  score = pack(s);
   return order64(s + (double)b + 0.0);
 }
 
 // Where more than 64 keys are equal or nearly equal: 64 experts at a time against
 // the slots so far, n_used rounds of maximum each.  Few registers, and slow.
-__device__ __forceinline__ void take_in_turn(const RouteArgs &a, int64_t t, int lane, int &id, float &sc) {
+__device__ __forceinline__ void take_in_turn(const RouteArgs &a, int64_t t, int lane, int &id, Score &sc) {
   uint64_t kept = 0;  // lane j: the key of slot j
   id = -1;
-  sc = 0.0f;
+  sc = 0;
 #pragma unroll 1
   for (int e0 = 0; e0 < a.n_expert; e0 += 64) {
     const int e = e0 + lane;
-    float score = 0.0f;
+    Score score = 0;
     uint64_t next = 0;
     if (e < a.n_expert) next = key_of(a, a.logits[t * a.n_expert + e], a.bias ? a.bias[e] : 0.0f, score);
     uint64_t old = kept, add = next;
@@ -200,10 +209,13 @@ __device__ __forceinline__ void take_in_turn(const RouteArgs &a, int64_t t, int 
       const int w = __builtin_amdgcn_ds_bpermute(l, was), n = __builtin_amdgcn_ds_bpermute(l, now);
       return from < 0 ? 0 : from < 64 ? w : n;
     };
+    auto pick64 = [&](uint64_t was, uint64_t now) {
+      const uint32_t lo = (uint32_t)pick((int)(uint32_t)was, (int)(uint32_t)now);
+      return (uint64_t)(uint32_t)pick((int)(was >> 32), (int)(now >> 32)) << 32 | lo;
+    };
     id = pick(id + 1, e + 1) - 1;
-    sc = __builtin_bit_cast(float, pick(__builtin_bit_cast(int, sc), __builtin_bit_cast(int, score)));
-    const uint32_t lo = (uint32_t)pick((int)(uint32_t)kept, (int)(uint32_t)next);
-    kept = (uint64_t)(uint32_t)pick((int)(kept >> 32), (int)(next >> 32)) << 32 | lo;
+    sc = pick64(sc, score);
+    kept = pick64(kept, next);
   }
 }
 
@@ -212,6 +224,7 @@ template <int EPL>
 __device__ __forceinline__ void route_token(const RouteArgs &a, int64_t t, int lane, int &id,
                                             float &weight) {
   const float inf = __builtin_huge_valf();
+  const bool softmax = a.scoring == kSoftmax;
   float z[EPL], b[EPL];
 #pragma unroll
   for (int i = 0; i < EPL; ++i) {
@@ -222,7 +235,8 @@ __device__ __forceinline__ void route_token(const RouteArgs &a, int64_t t, int l
   // Keys, or bounds of them: best reaches no higher than the lane's largest, upper no
   // lower than each.
   uint32_t upper[EPL], best = 0;
-  float sc, total = 1.0f, score = 0.0f;
+  float total = 1.0f;
+  Score slot, score = 0;
   uint64_t key = 0;  // one expert a lane is its own candidate
   if constexpr (EPL == 1) {
     key = key_of(a, z[0], b[0], score);
@@ -233,7 +247,7 @@ __device__ __forceinline__ void route_token(const RouteArgs &a, int64_t t, int l
       upper[i] = 0;
       if (i * 64 < a.n_expert && z[i] != -inf) {
         float s = z[i], off = 0.0f;
-        if (a.scoring != kSoftmax) {
+        if (!softmax) {
           s = score32(a.scoring, s);
           off = 0x1p-19f * (s + fabsf(b[i])) + 0x1p-62f;
         }
@@ -246,19 +260,20 @@ __device__ __forceinline__ void route_token(const RouteArgs &a, int64_t t, int l
   }
   const uint32_t border = border_of(best, a.n_used);
   if constexpr (EPL == 1) {
-    place(__ballot(best != 0 && best >= border), key, lane, score, a.n_used, lane, id, sc);
+    place(__ballot(best != 0 && best >= border), key, lane, score, softmax, a.n_used, lane, id, slot);
   } else {
     float zc = -inf, bc = 0.0f;
     int ec = 0;
     const int n = gather<EPL>(upper, border, z, b, lane, zc, bc, ec);
     if (n <= 64) {
       key = key_of(a, zc, bc, score);
-      place(n == 64 ? ~0ull : (1ull << n) - 1, key, ec, score, a.n_used, lane, id, sc);
+      place(n == 64 ? ~0ull : (1ull << n) - 1, key, ec, score, softmax, a.n_used, lane, id, slot);
     } else {
-      take_in_turn(a, t, lane, id, sc);
+      take_in_turn(a, t, lane, id, slot);
     }
   }
-  if (a.scoring == kSoftmax) {
+  if (softmax) {
+    const float sc = logit_of(slot);
     // exp(z - m) over the sum: m the largest chosen logit, or the largest of all
     // where the sum goes over all.  An order-preserving maximum keeps NaN.
     uint32_t top = id >= 0 ? order32(sc) : 0u;
@@ -277,8 +292,16 @@ __device__ __forceinline__ void route_token(const RouteArgs &a, int64_t t, int l
     weight = id >= 0 ? expf(sc - m) : 0.0f;
     total = wave_sum(a.renormalize ? weight : all);
   } else {
-    weight = id >= 0 ? sc : 0.0f;
+    weight = (float)score_of(slot);
     if (a.renormalize) total = wave_sum(weight);
+    if (a.renormalize && total < 0x1p-20f) {
+      // fp32 may hold a few bits of these scores, or none (a sigmoid of -88, of -104).
+      // Divided by the power of two of the largest first, they keep their weights.  From
+      // 2^-20 on what a score below 2^-126 loses is below 2^-129 of the sum.
+      const int top = (int)(wave_max(high(slot)) >> 20);
+      weight = (float)ldexp(score_of(slot), 1023 - top);
+      total = wave_sum(weight);
+    }
   }
   // A NaN sum must reach the weights; an empty row's zero sum must not.
   weight = (total == 0.0f ? weight : weight / total) * a.scale;
