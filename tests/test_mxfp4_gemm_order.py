@@ -8,6 +8,9 @@ a copy of stage k or of one before.
 Scale fetches are such operations too: a wait that leaves room for one is right only
 if the compiler kept the fetch behind the copies of its stage.
 
+A stage's copies go to the place of the stage RING before it, which every wave has read
+when it comes to the barrier behind that stage; they must not be issued before it.
+
 The kernels are compiled to assembly with the library's flags, and with other
 instruction schedulers as well, because an order that the source does not pin holds in
 one build only by chance; the operations, waits and barriers along every path through
@@ -77,12 +80,17 @@ def _paths(body):
     return _events(body[:first]), _events(body[first:last + 1]), tail
 
 
-def _check(events, copies_a_stage, where):
-    """Replays a wave's operations: reads behind barrier k find stages 0..k landed at it."""
-    queue, landed, at_barrier, stage = [], 0, 0, 0
+def _check(events, copies_a_stage, ring, where):
+    """Replays a wave's operations: reads behind barrier k find stages 0..k landed at it,
+    and copies of stage k + ring stand behind barrier k + 1."""
+    queue, issued, landed, at_barrier, stage = [], 0, 0, 0, 0
     for e in events:
         if e in ("copy", "load"):
             queue.append(e)
+            if e == "copy":
+                of = issued // copies_a_stage
+                assert of < ring or stage >= of - ring + 2, f"{where}: copy of stage {of} behind barrier {stage - 1}"
+                issued += 1
         elif e == "barrier":
             at_barrier, stage = landed, stage + 1
         elif e == "read":
@@ -113,7 +121,7 @@ def test_a_stage_has_landed_at_its_barrier(scheduler, tmp_path):
         assert loop.count("copy") == 4 * copies and loop.count("barrier") == 4, where
         assert tail.count("copy") == (2 * copies if tm * tn <= 4 else 0), where
         for times in range(4):
-            stages = _check(front + times * loop + tail, copies, where)
+            stages = _check(front + times * loop + tail, copies, ring, where)
             assert stages == 1 + 4 * times + tail.count("barrier")
 
 
@@ -122,6 +130,12 @@ def test_the_model_sees_a_fetch_in_front_of_its_copies():
     front = ["copy"] * 4 + [2, "barrier"]
     good = [0, "barrier", "read", "copy", "copy", "load", 1, "barrier", "read"]
     bad = [0, "barrier", "read", "load", "copy", "copy", 1, "barrier", "read"]
-    assert _check(front + good, 2, "good") == 3
-    with pytest.raises(AssertionError):
-        _check(front + bad, 2, "bad")
+    assert _check(front + good, 2, 2, "good") == 3
+    with pytest.raises(AssertionError, match="landed"):
+        _check(front + bad, 2, 2, "bad")
+
+
+def test_the_model_sees_a_copy_into_a_place_that_is_still_read():
+    front = ["copy"] * 4 + [2, "barrier", "read"]
+    with pytest.raises(AssertionError, match="copy of stage 2"):
+        _check(front + ["copy", "copy", 0, "barrier", "read"], 2, 2, "bad")
