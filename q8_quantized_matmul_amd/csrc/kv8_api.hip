@@ -1,0 +1,176 @@
+// kv8_api.hip -- the C ABI of include/kv8.h: host-side argument checks and
+// launches on the caller's stream.  Nothing here allocates device memory.
+#include <math.h>
+#include <stdint.h>
+
+#include "kv8.h"
+#include "kv8_launch.h"
+#include "launch.h"
+
+static_assert(KV8_F32 == kv::kF32 && KV8_BF16 == kv::kBF16 && KV8_F16 == kv::kF16,
+              "header and library agree on the element types");
+
+namespace {
+
+bool aligned(const void *p, uintptr_t a) { return (reinterpret_cast<uintptr_t>(p) & (a - 1)) == 0; }
+bool type_ok(int32_t t) { return t == KV8_F32 || t == KV8_BF16 || t == KV8_F16; }
+int type_size(int32_t t) { return t == KV8_F32 ? 4 : 2; }
+int status_of(hipError_t e) { return e == hipSuccess ? Q8_0_OK : Q8_0_ELAUNCH; }
+
+// log2 of a power of two in [lo, hi], or -1.
+int log_of(int64_t v, int64_t lo, int64_t hi) {
+  if (v < lo || v > hi || (v & (v - 1)) != 0) return -1;
+  int n = 0;
+  while ((int64_t{1} << n) < v) ++n;
+  return n;
+}
+
+constexpr int64_t kMaxSeq = 1 << 20, kMaxTok = 1 << 24, kMaxStride = int64_t{1} << 40;
+// A launch has fewer than 2^32 threads: attention makes a workgroup of 256 for 16 rows and head.
+constexpr int64_t kMaxRows = int64_t{1} << 27, kMaxSeqHeads = int64_t{1} << 22;
+constexpr int32_t kMaxKvHeads = 4096, kMaxHeads = 1 << 14;
+
+int read_cache(const kv8_cache *c, kv::Cache *out) {
+  if (!c || c->n_pages < 1 || c->n_pages > INT32_MAX || c->n_kv < 1 || c->n_kv > kMaxKvHeads) return Q8_0_EINVAL;
+  if (c->head_dim != 64 && c->head_dim != 128 && c->head_dim != 192 && c->head_dim != 256 && c->head_dim != 512)
+    return Q8_0_EINVAL;
+  const int page_log = log_of(c->page_size, 16, 1024);
+  const int block_log = page_log < 0 ? -1 : log_of(c->block, 16, c->page_size < 128 ? c->page_size : 128);
+  if (block_log < 0) return Q8_0_EINVAL;
+  *out = {static_cast<int8_t *>(c->k_codes), static_cast<int8_t *>(c->v_codes), c->k_scales, c->v_scales,
+          (int32_t)c->n_pages, c->n_kv, c->head_dim, page_log, block_log};
+  return Q8_0_OK;
+}
+
+int read_batch(const kv8_batch *b, const kv::Cache &c, kv::Batch *out) {
+  if (!b || b->n_seq < 0 || b->n_seq > kMaxSeq || b->n_tok < 0 || b->n_tok > kMaxTok || b->table_width < 0 ||
+      b->table_width > (INT32_MAX >> c.page_log) || b->max_new < 0 || b->max_len < 0 || b->n_seq * c.n_kv > kMaxSeqHeads)
+    return Q8_0_EINVAL;
+  if (!b->starts && b->n_tok != b->n_seq) return Q8_0_EINVAL;
+  const int64_t room = b->table_width << c.page_log;
+  const int64_t max_new = b->starts ? (b->max_new < b->n_tok ? b->max_new : b->n_tok) : 1;
+  const int64_t max_len = b->max_len && b->max_len < room ? b->max_len : room;
+  *out = {b->page_table, b->lens, b->starts, (int32_t)b->n_seq, (int32_t)b->n_tok, (int32_t)b->table_width,
+          (int32_t)max_new, (int32_t)max_len};
+  return Q8_0_OK;
+}
+
+bool nothing_to_do(const kv::Batch &b) { return b.n_seq == 0 || b.n_tok == 0 || b.max_new == 0; }
+
+// Pointers of a cache and a batch with work to do.
+int check_pointers(const kv::Cache &c, const kv::Batch &b) {
+  if (!c.k || !c.v || !c.ks || !c.vs || !b.lens || (!b.table && b.width > 0)) return Q8_0_EINVAL;
+  if (!aligned(c.k, 16) || !aligned(c.v, 16) || !aligned(c.ks, 4) || !aligned(c.vs, 4) || !aligned(b.table, 4) ||
+      !aligned(b.lens, 4) || !aligned(b.starts, 4))
+    return Q8_0_EALIGN;
+  return Q8_0_OK;
+}
+
+int read_rows(const void *p, int64_t token_stride, int64_t head_stride, int32_t type, kv::Rows *out) {
+  if (!type_ok(type) || token_stride < 0 || head_stride < 0 || token_stride > kMaxStride || head_stride > kMaxStride)
+    return Q8_0_EINVAL;
+  if (!p) return Q8_0_EINVAL;
+  if (!aligned(p, type_size(type))) return Q8_0_EALIGN;
+  const int per16 = 16 / type_size(type);
+  *out = {p, token_stride, head_stride, type,
+          aligned(p, 16) && token_stride % per16 == 0 && head_stride % per16 == 0};
+  return Q8_0_OK;
+}
+
+}  // namespace
+
+namespace kv {
+
+size_t partial_bytes(const Cache &c, const Batch &b, int n_q, int splits) {
+  return splits > 1 ? (size_t)splits * b.n_tok * n_q * (c.d + 1) * sizeof(float) : 0;
+}
+
+// Splits: two workgroups for each of the 256 compute units, none with less than 128 keys.
+Plan attention_plan(const Cache &c, const Batch &b, int n_q, bool halves, size_t ws_bytes) {
+  const int group = n_q / c.n_kv;
+  const int64_t tiles = (int64_t)b.max_new * group > 16 ? (int64_t)b.n_tok * group / 16 + b.n_seq : b.n_seq;
+  const int64_t units = tiles * c.n_kv;
+  int64_t splits = (512 + units - 1) / units;
+  const int64_t most = (b.max_len + 127) / 128;
+  if (splits > most) splits = most;
+  if (splits > 256) splits = 256;
+  while (splits > 1 && partial_bytes(c, b, n_q, (int)splits) > ws_bytes) --splits;
+  return {false, splits < 1 ? 1 : (int)splits};
+}
+
+}  // namespace kv
+
+extern "C" {
+
+int kv8_write(const kv8_cache *cache, const kv8_batch *batch, const void *k, int64_t k_token_stride,
+              int64_t k_head_stride, const void *v, int64_t v_token_stride, int64_t v_head_stride,
+              int32_t type, hipStream_t stream) {
+  kv::Cache c;
+  kv::Batch b;
+  kv::Rows kr, vr;
+  int st = read_cache(cache, &c);
+  if (st == Q8_0_OK) st = read_batch(batch, c, &b);
+  if (st != Q8_0_OK || !type_ok(type)) return Q8_0_EINVAL;
+  if (nothing_to_do(b)) return Q8_0_OK;
+  if ((st = check_pointers(c, b)) != Q8_0_OK || (st = read_rows(k, k_token_stride, k_head_stride, type, &kr)) != Q8_0_OK ||
+      (st = read_rows(v, v_token_stride, v_head_stride, type, &vr)) != Q8_0_OK)
+    return st;
+  if ((st = q8::check_device()) != Q8_0_OK) return st;
+  return status_of(kv::launch_write(c, b, kr, vr, stream));
+}
+
+int kv8_read(const kv8_cache *cache, const kv8_batch *batch, void *k, void *v, int32_t type,
+             hipStream_t stream) {
+  kv::Cache c;
+  kv::Batch b;
+  int st = read_cache(cache, &c);
+  if (st == Q8_0_OK) st = read_batch(batch, c, &b);
+  if (st != Q8_0_OK || !type_ok(type)) return Q8_0_EINVAL;
+  if (nothing_to_do(b) || (!k && !v)) return Q8_0_OK;
+  if ((st = check_pointers(c, b)) != Q8_0_OK) return st;
+  if (!aligned(k, 16) || !aligned(v, 16)) return Q8_0_EALIGN;
+  if ((st = q8::check_device()) != Q8_0_OK) return st;
+  return status_of(kv::launch_read(c, b, k, v, type, stream));
+}
+
+size_t kv8_attention_workspace_bytes(const kv8_cache *cache, const kv8_batch *batch, int32_t n_q) {
+  kv::Cache c;
+  kv::Batch b;
+  if (read_cache(cache, &c) != Q8_0_OK || read_batch(batch, c, &b) != Q8_0_OK || n_q < 1 || n_q > kMaxHeads ||
+      n_q % c.n_kv != 0 || (int64_t)b.n_tok * n_q > kMaxRows || nothing_to_do(b))
+    return 0;
+  size_t most = 0;
+  for (bool halves : {false, true}) {
+    const kv::Plan p = kv::attention_plan(c, b, n_q, halves, SIZE_MAX);
+    const size_t bytes = kv::partial_bytes(c, b, n_q, p.splits);
+    if (bytes > most) most = bytes;
+  }
+  return most;
+}
+
+int kv8_attention(const kv8_cache *cache, const kv8_batch *batch, const kv8_attention_args *args,
+                  void *workspace, size_t workspace_bytes, hipStream_t stream) {
+  kv::Cache c;
+  kv::Batch b;
+  int st = read_cache(cache, &c);
+  if (st == Q8_0_OK) st = read_batch(batch, c, &b);
+  if (st != Q8_0_OK || !args) return Q8_0_EINVAL;
+  const kv8_attention_args &x = *args;
+  if (x.n_q < 1 || x.n_q > kMaxHeads || x.n_q % c.n_kv != 0 || x.window < 0 || !isfinite(x.scale) ||
+      !type_ok(x.out_type) || !type_ok(x.q_type) || (int64_t)b.n_tok * x.n_q > kMaxRows)
+    return Q8_0_EINVAL;
+  if (nothing_to_do(b)) return Q8_0_OK;
+  kv::Attention a{x.out, {}, x.out_type, x.n_q, x.n_q / c.n_kv, x.window, x.scale, x.sinks, x.lse};
+  if ((st = check_pointers(c, b)) != Q8_0_OK || (st = read_rows(x.q, x.q_token_stride, x.q_head_stride, x.q_type, &a.q)) != Q8_0_OK)
+    return st;
+  if (!x.out) return Q8_0_EINVAL;
+  if (!aligned(x.out, 16) || !aligned(x.sinks, 4) || !aligned(x.lse, 4) || !aligned(workspace, 16)) return Q8_0_EALIGN;
+  if ((st = q8::check_device()) != Q8_0_OK) return st;
+  const bool halves = x.q_type == KV8_F32 || x.out_type == KV8_F32;
+  const kv::Plan p = kv::attention_plan(c, b, x.n_q, halves, workspace ? workspace_bytes : 0);
+  hipError_t e = kv::launch_stream(c, b, a, p.splits, workspace, stream);
+  if (e == hipSuccess && p.splits > 1) e = kv::launch_join(c, b, a, p.splits, workspace, stream);
+  return status_of(e);
+}
+
+}  // extern "C"

@@ -1,0 +1,320 @@
+// kv8_stream.hip -- attention for few query rows a key/value head (single tokens, drafts):
+// the cache streams through, straight from HBM into matrix operands.
+//
+// A workgroup takes 16 query rows that share a key/value head (tokens x the head's query heads) and
+// a stretch of their keys; its four waves take 32 keys each in turn and meet at the end.  Per
+// step a wave multiplies 32 keys by its 16 rows, S^T = K Q^T, on v_mfma_f32_16x16x32_f16:
+// transposed, so that a lane's results are 4 + 4 keys of one row, which is how the second
+// product, O^T = V^T P^T, takes its weights: they never leave the lane.  The codes of 16 keys lie as
+// that instruction's operand takes them, so every load of a wave is 1024 adjacent bytes (K) or
+// four runs of 256 (V) and there is no LDS in the loop.
+// What bounds it is HBM: 2 * d bytes a key, 160 VALU instructions a lane for the codes of 32 keys
+// of 128 values (8 KB) beside 16 matrix instructions.
+#include "kv8_attn.h"
+
+namespace kv {
+namespace {
+
+constexpr int kRows = 16, kStep = 32, kWaves = 4;
+
+template <int D, bool HALVES>
+__global__ __launch_bounds__(256) void stream_kernel(Cache c, Batch b, Attention a, int splits, void *ws) {
+  constexpr int kChunks = D / 64;
+  __shared__ float join_o[kWaves][64][kRows + 1];
+  __shared__ float join_m[kWaves][kRows], join_l[kWaves][kRows];
+  __shared__ int join_e[kWaves];
+  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+  const int g = lane >> 4, col = lane & 15;
+  const int head = blockIdx.x % c.n_kv, w = blockIdx.x / c.n_kv, split = blockIdx.y;
+
+  // the rows
+  int s = w, tile = 0;
+  if ((int64_t)b.max_new * a.group > kRows) {
+    const Slots slots{kRows, a.group, 1};
+    s = find_sequence(b, slots, w);
+    tile = (int)(w - slots.first(b, s));
+  }
+  const Span q = span_of(b, c, s);
+  const int rows = q.n * a.group, r0 = tile * kRows;
+  if (r0 >= rows) return;
+  const int tok_hi = (min(r0 + kRows, rows) - 1) / a.group;
+  const int row = r0 + col, tok = min(row / a.group, tok_hi);
+  const bool row_ok = row < rows;
+  const int q_head = head * a.group + (row_ok ? row - tok * a.group : 0);
+  const int pos = row_ok ? q.first + tok : -1;
+  const int pos_lo = q.first + r0 / a.group, pos_hi = q.first + tok_hi;
+
+  // the keys: steps [st, st_end) of 32 from key0 on
+  const int key0 = a.window ? max(pos_lo - a.window + 1, 0) & ~(kStep - 1) : 0;
+  const int key_end = pos_hi + 1;
+  const int steps = max(key_end - key0 + kStep - 1, 0) / kStep;
+  const int per = (steps + splits - 1) / splits;
+  const int st_end = min(steps, (split + 1) * per);
+  const int st_begin = split * per + wave;
+
+  // query operands: lane (g, col) holds dims 64 c + 16 g + 0 .. 15 of row col, as K's 16-dim chunks lie
+  h8 qh[2 * kChunks], ql[HALVES ? 2 * kChunks : 1];
+  float factor;
+  {
+    float v[kChunks][16], amax = 0.f;
+    const int64_t at = (int64_t)(q.row0 + tok) * a.q.token_stride + (int64_t)q_head * a.q.head_stride + 16 * g;
+#pragma unroll
+    for (int i = 0; i < kChunks; ++i) {
+      load_row<16>(a.q, at + 64 * i, v[i]);
+#pragma unroll
+      for (int j = 0; j < 16; ++j) amax = as<float>(max(as<uint32_t>(amax), as<uint32_t>(v[i][j]) & 0x7fffffffu));
+    }
+    amax = as<float>(max(as<uint32_t>(amax), (uint32_t)__shfl_xor(as<int>(amax), 16)));
+    amax = as<float>(max(as<uint32_t>(amax), (uint32_t)__shfl_xor(as<int>(amax), 32)));
+    const RowScale rs(amax, a.scale);
+    factor = rs.factor;
+#pragma unroll
+    for (int i = 0; i < kChunks; ++i)
+#pragma unroll
+      for (int j = 0; j < 16; ++j) {
+        const float x = ldexp_fast(v[i][j], -rs.e);
+        const _Float16 hi = (_Float16)x;
+        qh[2 * i + (j >> 3)][j & 7] = hi;
+        if constexpr (HALVES) ql[2 * i + (j >> 3)][j & 7] = (_Float16)(x - (float)hi);
+      }
+  }
+
+  f32x4 o[4 * kChunks];
+#pragma unroll
+  for (int i = 0; i < 4 * kChunks; ++i) o[i] = f32x4{0.f, 0.f, 0.f, 0.f};
+  float m = kLowest, l = 0.f;
+  int e = kNoScale;
+
+  for (int chunk = st_begin; chunk < st_end; chunk += 32 * kWaves) {
+    // pages and scales of this wave's next 32 steps: lane i looks up 16 keys, step i / 2, half i & 1
+    int page = 0, exponent = kNoScale;
+    float ks = 0.f, vs = 0.f;
+    {
+      const int st = chunk + (lane >> 1) * kWaves;
+      const int key = key0 + st * kStep + 16 * (lane & 1);
+      if (st < st_end && key < key_end) {
+        page = page_of(c, b, s, key);
+        if (page >= 0) {
+          const int64_t at = scale_offset(c, page, head, key);
+          ks = c.ks[at];
+          vs = c.vs[at];
+          if (vs != 0.f) exponent = exponent_of(vs);
+        } else {
+          page = 0;
+          ks = vs = as<float>(0x7fc00000u);
+        }
+      }
+    }
+    const int n = min((st_end - chunk + kWaves - 1) / kWaves, 32);
+    for (int t = 0; t < n; ++t) {
+      const int key = key0 + (chunk + t * kWaves) * kStep;
+      u32x4 kc[2][kChunks], vc[2][kChunks];
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {
+        const int64_t at = code_offset(c, __builtin_amdgcn_readlane(page, 2 * t + h), head, key + 16 * h);
+        const int8_t *kp = c.k + at + 16 * lane, *vp = c.v + at + g * 4 * D + 16 * col;
+#pragma unroll
+        for (int i = 0; i < kChunks; ++i) {
+          kc[h][i] = *reinterpret_cast<const u32x4 *>(kp + 1024 * i);
+          vc[h][i] = *reinterpret_cast<const u32x4 *>(vp + 256 * i);
+        }
+      }
+      float x[2][4];
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {
+        f32x4 z = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+        for (int i = 0; i < kChunks; ++i) {
+          const h8 k0 = codes_f16(kc[h][i][0], kc[h][i][1]), k1 = codes_f16(kc[h][i][2], kc[h][i][3]);
+          z = mfma16(k0, qh[2 * i], z);
+          z = mfma16(k1, qh[2 * i + 1], z);
+          if constexpr (HALVES) {
+            z = mfma16(k0, ql[2 * i], z);
+            z = mfma16(k1, ql[2 * i + 1], z);
+          }
+        }
+        const float f = as<float>(__builtin_amdgcn_readlane(as<int>(ks), 2 * t + h)) * factor;
+#pragma unroll
+        for (int i = 0; i < 4; ++i) x[h][i] = z[i] * f;
+      }
+      // keys that not every row sees
+      const bool ragged = key + kStep - 1 > pos_lo || (a.window && key <= pos_hi - a.window);
+      if (ragged) {
+#pragma unroll
+        for (int h = 0; h < 2; ++h)
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            const int j = key + 16 * h + 4 * g + i;
+            if (j > pos || (a.window && j <= pos - a.window)) x[h][i] = -INFINITY;
+          }
+      }
+      float top = x[0][0];
+#pragma unroll
+      for (int i = 1; i < 8; ++i) top = fmaxf(top, x[i >> 2][i & 3]);
+      if (__any(top > m + kSlack)) {
+        top = fmaxf(top, __shfl_xor(top, 16));
+        top = fmaxf(top, __shfl_xor(top, 32));
+        const float was = m;
+        m = fmaxf(m, top);
+        const float f = exp2_fast(was - m);
+        l *= f;
+#pragma unroll
+        for (int i = 0; i < 4 * kChunks; ++i) o[i] *= f;
+      }
+      const int e2 = max(__builtin_amdgcn_readlane(exponent, 2 * t), __builtin_amdgcn_readlane(exponent, 2 * t + 1));
+      if (e2 > e) {
+        const float f = ldexp_fast(1.f, e - e2);
+        e = e2;
+#pragma unroll
+        for (int i = 0; i < 4 * kChunks; ++i) o[i] *= f;
+      }
+      h8 ph, pl;
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {
+        const float v = ldexp_fast(as<float>(__builtin_amdgcn_readlane(as<int>(vs), 2 * t + h)), -e);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          const float p = exp2_fast(x[h][i] - (m - kBias));
+          l += p;
+          float y = p * v;
+          if (ragged && x[h][i] == -INFINITY) y = 0.f;  // also where v is not finite
+          ph[4 * h + i] = (_Float16)y;
+          if constexpr (HALVES) pl[4 * h + i] = (_Float16)(y - (float)ph[4 * h + i]);
+        }
+      }
+#pragma unroll
+      for (int i = 0; i < 4 * kChunks; ++i) {
+        const h8 v = codes_f16(vc[0][i >> 2][i & 3], vc[1][i >> 2][i & 3]);
+        o[i] = mfma16(v, ph, o[i]);
+        if constexpr (HALVES) o[i] = mfma16(v, pl, o[i]);
+      }
+    }
+  }
+
+  // the four waves' sums, 64 dims at a time; a thread takes 4 dims of one row
+  l += __shfl_xor(l, 16);
+  l += __shfl_xor(l, 32);
+  if (g == 0) {
+    join_m[wave][col] = m;
+    join_l[wave][col] = l;
+  }
+  if (lane == 0) join_e[wave] = e;
+  __syncthreads();
+  const int jr = threadIdx.x >> 4, jd = (threadIdx.x & 15) * 4;
+  float jm = kLowest, jl = 0.f, jf[kWaves];
+  int je = kNoScale;
+#pragma unroll
+  for (int i = 0; i < kWaves; ++i) {
+    jm = fmaxf(jm, join_m[i][jr]);
+    je = max(je, join_e[i]);
+  }
+#pragma unroll
+  for (int i = 0; i < kWaves; ++i) {
+    const float f = exp2_fast(join_m[i][jr] - jm);
+    jl += join_l[i][jr] * f;
+    jf[i] = ldexp_fast(f, join_e[i] - je);
+  }
+  const int j_row = r0 + jr, j_tok = j_row / a.group, j_head = head * a.group + j_row % a.group;
+  const bool j_ok = j_row < rows;
+  const int64_t j_at = (int64_t)(q.row0 + j_tok) * a.n_q + j_head;  // row of the outputs
+  const float sink2 = splits == 1 && a.sinks && j_ok ? a.sinks[j_head] * kLog2e : -INFINITY;
+  const Finish fin(jm, jl, je, sink2);
+  const Partials part(ws, b, c, a.n_q, splits);
+  if (j_ok && jd == 0) {
+    if (splits > 1)
+      part.lse2[split * part.rows + j_at] = fin.lse2;
+    else if (a.lse)
+      a.lse[j_at] = fin.lse2 * kLn2;
+  }
+#pragma unroll
+  for (int i = 0; i < kChunks; ++i) {
+    if (i) __syncthreads();
+#pragma unroll
+    for (int j = 0; j < 4; ++j)
+#pragma unroll
+      for (int k = 0; k < 4; ++k) join_o[wave][16 * g + 4 * k + j][col] = o[4 * i + j][k];
+    __syncthreads();
+    float v[4];
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      float sum = 0.f;
+#pragma unroll
+      for (int k = 0; k < kWaves; ++k) sum += join_o[k][jd + j][jr] * jf[k];
+      v[j] = jl == 0.f ? 0.f : sum * fin.factor;
+    }
+    if (j_ok) {
+      if (splits > 1)
+        store_values<kF32, 4>(part.out, (split * part.rows + j_at) * D + 64 * i + jd, v);
+      else
+        store_row<4>(a.out, a.out_type, j_at * D + 64 * i + jd, v);
+    }
+  }
+}
+
+// out[row] = sum over splits of out_s * exp2(lse2_s) / (their sum, and the sink's); splits in order.
+// A thread takes 4 dims of a row.
+__global__ __launch_bounds__(256) void join_kernel(Cache c, Batch b, Attention a, int splits, const void *ws) {
+  const Partials part(const_cast<void *>(ws), b, c, a.n_q, splits);
+  const int lanes = c.d / 4;
+  const int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x;
+  const int64_t row = i / lanes;
+  const int at = (int)(i - row * lanes) * 4;
+  const int tok = (int)(row / a.n_q), head = (int)(row - (int64_t)tok * a.n_q);
+  if (row >= part.rows || tok < start_of(b, 0) || tok >= (b.starts ? start_of(b, b.n_seq) : b.n_seq)) return;
+  float top = -INFINITY;
+  bool nan = false;
+  for (int s = 0; s < splits; ++s) {
+    const float z = part.lse2[s * part.rows + row];
+    top = fmaxf(top, z);
+    nan |= z != z;
+  }
+  float sum = 0.f, v[4] = {0.f, 0.f, 0.f, 0.f};
+  if (top > -INFINITY || nan) {
+    for (int s = 0; s < splits; ++s) {
+      const float z = part.lse2[s * part.rows + row];
+      if (z == -INFINITY) continue;
+      const float f = exp2_fast(z - top);
+      const f32x4 x = *reinterpret_cast<const f32x4 *>(part.out + (s * part.rows + row) * c.d + at);
+      sum += f;
+#pragma unroll
+      for (int j = 0; j < 4; ++j) v[j] += x[j] * f;
+    }
+  }
+  // weights relative to the largest: a sum of them is a sum of kBias more
+  Finish fin(top + kBias, sum, 0, a.sinks ? a.sinks[head] * kLog2e : -INFINITY);
+#pragma unroll
+  for (int j = 0; j < 4; ++j) v[j] = sum == 0.f ? 0.f : v[j] * fin.factor;
+  store_row<4>(a.out, a.out_type, row * c.d + at, v);
+  if (at == 0 && a.lse) a.lse[row] = fin.lse2 * kLn2;
+}
+
+template <int D>
+hipError_t launch_dim(const Cache &c, const Batch &b, const Attention &a, int splits, void *ws, hipStream_t s) {
+  const int64_t tiles = (int64_t)b.max_new * a.group > kRows ? (int64_t)b.n_tok * a.group / kRows + b.n_seq : b.n_seq;
+  const dim3 grid((uint32_t)(tiles * c.n_kv), (uint32_t)splits);
+  if (a.q.type == kF32 || a.out_type == kF32)
+    stream_kernel<D, true><<<grid, 256, 0, s>>>(c, b, a, splits, ws);
+  else
+    stream_kernel<D, false><<<grid, 256, 0, s>>>(c, b, a, splits, ws);
+  return hipGetLastError();
+}
+
+}  // namespace
+
+hipError_t launch_stream(const Cache &c, const Batch &b, const Attention &a, int splits, void *ws, hipStream_t s) {
+  switch (c.d) {
+    case 64: return launch_dim<64>(c, b, a, splits, ws, s);
+    case 128: return launch_dim<128>(c, b, a, splits, ws, s);
+    case 192: return launch_dim<192>(c, b, a, splits, ws, s);
+    case 256: return launch_dim<256>(c, b, a, splits, ws, s);
+    default: return launch_dim<512>(c, b, a, splits, ws, s);
+  }
+}
+
+hipError_t launch_join(const Cache &c, const Batch &b, const Attention &a, int splits, const void *ws, hipStream_t s) {
+  const int64_t threads = (int64_t)b.n_tok * a.n_q * (c.d / 4);
+  join_kernel<<<dim3((uint32_t)((threads + 255) / 256)), 256, 0, s>>>(c, b, a, splits, ws);
+  return hipGetLastError();
+}
+
+}  // namespace kv
