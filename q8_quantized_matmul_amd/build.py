@@ -15,7 +15,7 @@ LIB = os.path.join(PKG, "libq8_0.so")
 SOURCES = ["api.hip", "quantize.hip", "matvec.hip", "moe.hip", "gemm.hip", "skinny.hip", "probe.hip",
            "debug.hip", "mxfp4_api.hip", "mxfp4_quantize.hip",
            "mxfp4_matmul.hip", "mxfp4_gemm.hip", "mxfp4_moe.hip", "moe_topk.hip",
-           "kv8_api.hip", "kv8_write.hip", "kv8_stream.hip"]
+           "kv8_api.hip", "kv8_write.hip", "kv8_stream.hip", "kv8_tile.hip"]
 
 # -packed-fp32-ops: keep the compiler from emitting packed fp32 VALU forms.
 # No fast-math: the quantizer relies on IEEE division and roundf.

@@ -85,17 +85,22 @@ size_t partial_bytes(const Cache &c, const Batch &b, int n_q, int splits) {
   return splits > 1 ? (size_t)splits * b.n_tok * n_q * (c.d + 1) * sizeof(float) : 0;
 }
 
-// Splits: two workgroups for each of the 256 compute units, none with less than 128 keys.
+// The tiled kernel for more than 16 rows a sequence and key/value head, but for heads of 512
+// in two halves, whose operands do not fit its registers.
+// Splits: workgroups for each of the 256 compute units, none with less than 128 keys.
 Plan attention_plan(const Cache &c, const Batch &b, int n_q, bool halves, size_t ws_bytes) {
   const int group = n_q / c.n_kv;
-  const int64_t tiles = (int64_t)b.max_new * group > 16 ? (int64_t)b.n_tok * group / 16 + b.n_seq : b.n_seq;
+  const int64_t most_rows = (int64_t)b.max_new * group;
+  const bool tiled = most_rows > 16 && !(halves && c.d > 256);
+  const int rows = tiled ? tile_rows(c.d) : 16;
+  const int64_t tiles = most_rows > rows ? (int64_t)b.n_tok * group / rows + b.n_seq : b.n_seq;
   const int64_t units = tiles * c.n_kv;
   int64_t splits = (512 + units - 1) / units;
   const int64_t most = (b.max_len + 127) / 128;
   if (splits > most) splits = most;
   if (splits > 256) splits = 256;
   while (splits > 1 && partial_bytes(c, b, n_q, (int)splits) > ws_bytes) --splits;
-  return {false, splits < 1 ? 1 : (int)splits};
+  return {tiled, splits < 1 ? 1 : (int)splits};
 }
 
 }  // namespace kv
@@ -168,7 +173,8 @@ int kv8_attention(const kv8_cache *cache, const kv8_batch *batch, const kv8_atte
   if ((st = q8::check_device()) != Q8_0_OK) return st;
   const bool halves = x.q_type == KV8_F32 || x.out_type == KV8_F32;
   const kv::Plan p = kv::attention_plan(c, b, x.n_q, halves, workspace ? workspace_bytes : 0);
-  hipError_t e = kv::launch_stream(c, b, a, p.splits, workspace, stream);
+  hipError_t e = p.tiled ? kv::launch_tile(c, b, a, p.splits, workspace, stream)
+                         : kv::launch_stream(c, b, a, p.splits, workspace, stream);
   if (e == hipSuccess && p.splits > 1) e = kv::launch_join(c, b, a, p.splits, workspace, stream);
   return status_of(e);
 }

@@ -30,6 +30,16 @@ __device__ __forceinline__ f32x16 mfma32(h8 a, h8 b, f32x16 c) {
   return __builtin_amdgcn_mfma_f32_32x32x16_f16(a, b, c, 0, 0, 0);
 }
 
+// f with the type as a constant.
+template <class F>
+__device__ __forceinline__ auto by_type(int type, F f) {
+  switch (type) {
+    case kF32: return f(std::integral_constant<int, kF32>());
+    case kBF16: return f(std::integral_constant<int, kBF16>());
+    default: return f(std::integral_constant<int, kF16>());
+  }
+}
+
 template <int N>
 __device__ __forceinline__ void load_row(const Rows &r, int64_t at, float (&v)[N]) {
   switch (r.type) {

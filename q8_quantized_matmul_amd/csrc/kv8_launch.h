@@ -53,6 +53,10 @@ struct Plan {
 Plan attention_plan(const Cache &c, const Batch &b, int n_q, bool halves, size_t ws_bytes);
 size_t partial_bytes(const Cache &c, const Batch &b, int n_q, int splits);
 
+// kv8_tile.hip; tile_rows: query rows of a workgroup
+int tile_rows(int d);
+hipError_t launch_tile(const Cache &c, const Batch &b, const Attention &a, int splits, void *ws, hipStream_t s);
+
 // kv8_stream.hip
 hipError_t launch_stream(const Cache &c, const Batch &b, const Attention &a, int splits, void *ws, hipStream_t s);
 // out and lse of the partial results.
