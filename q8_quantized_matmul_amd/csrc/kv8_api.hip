@@ -92,7 +92,7 @@ Plan attention_plan(const Cache &c, const Batch &b, int n_q, bool halves, size_t
   const int group = n_q / c.n_kv;
   const int64_t most_rows = (int64_t)b.max_new * group;
   const bool tiled = most_rows > 16 && !(halves && c.d > 256);
-  const int rows = tiled ? tile_rows(c.d) : 16;
+  const int rows = tiled ? tile_rows(c.d, halves) : 16;
   const int64_t tiles = most_rows > rows ? (int64_t)b.n_tok * group / rows + b.n_seq : b.n_seq;
   const int64_t units = tiles * c.n_kv;
   int64_t splits = (512 + units - 1) / units;

@@ -54,7 +54,7 @@ Plan attention_plan(const Cache &c, const Batch &b, int n_q, bool halves, size_t
 size_t partial_bytes(const Cache &c, const Batch &b, int n_q, int splits);
 
 // kv8_tile.hip; tile_rows: query rows of a workgroup
-int tile_rows(int d);
+int tile_rows(int d, bool halves);
 hipError_t launch_tile(const Cache &c, const Batch &b, const Attention &a, int splits, void *ws, hipStream_t s);
 
 // kv8_stream.hip

@@ -3,53 +3,64 @@
 //
 // A workgroup takes 32 query rows a wave (tokens x the head's query heads) and a stretch of their
 // keys, kKeys at a time (heads of 512: two waves share 32 rows, half of the dims each, and add
-// their scores through LDS; a wave could not hold the sums and queries of 512 dims).  Codes come from HBM or L2 as int8, become fp16 once in the workgroup
-// and lie in LDS in the order of the matrix operands, so that every operand is one conflict-free
-// 16-byte read a lane.  Both products run on v_mfma_f32_32x32x16_f16, transposed (S^T = K Q^T,
-// O^T = V^T P^T): a lane then holds 16 of 32 keys of one row, its weights become the second product's
-// operand without leaving the lane, and a row's running bound and sum are one register each.
-// Two LDS buffers and one barrier a tile: while the waves multiply tile t, tile t + 1 is written to
-// the other buffer from registers and tile t + 2 is on its way from memory.
+// their scores through LDS; a wave could not hold the sums and queries of 512 dims).  Codes come
+// from HBM or L2 as int8, become fp16 once in the workgroup and lie in LDS in the order of the
+// matrix operands, so that every operand is one conflict-free 16-byte read a lane.  Both products
+// run on v_mfma_f32_32x32x16_f16, transposed (S^T = K Q^T, O^T = V^T P^T): a lane then holds 16 of
+// 32 keys of one row, its weights become the second product's operand without leaving the lane, and
+// a row's running bound and sum are one register each.
+//
+// The matrix core and the vector ALU have about equal work (of 64 keys and 32 rows of 128 values: 32
+// instructions of 32 cycles; 32 exp2 and 200 others), so a wave does both at once: in step t it
+// multiplies the keys of tile t + 1 while it turns the scores of tile t into weights, then the values of tile
+// t while it scales the scores of t + 1 and puts the tiles that come next into LDS.  K is therefore staged
+// a tile ahead of V; each has two buffers, and there is one barrier a step.
 #include "kv8_attn.h"
 
 namespace kv {
 namespace {
 
-// Keys of a tile, waves of a workgroup.
-template <int D>
+// Scales of V this many powers of two below the largest are not folded into the exponent (put).
+constexpr int kFoldBits = 8, kNoFold = -100000;
+
+// The largest sum of a lane's weights of a tile: none is above fp16's 65504 then.
+constexpr float kMostSum = 0x1p15f;
+
+// In a branch that is hardly ever taken: what follows is not to be computed ahead of it.
+__device__ __forceinline__ void rare() { asm volatile(""); }
+
+template <int D, bool HALVES>
 struct Shape {
-  static constexpr int kKeys = D <= 128 ? 64 : 32;
-  static constexpr int kWaves = 4;
+  static constexpr int kKeys = D <= 128 ? 64 : 32;         // of a tile
+  static constexpr int kWaves = D <= 128 && !HALVES ? 8 : 4;
   static constexpr int kParts = D > 256 ? 2 : 1;           // waves that share 32 rows
   static constexpr int kDims = D / kParts;                 // dims of a wave
   static constexpr int kThreads = 64 * kWaves;
   static constexpr int kRows = 32 * kWaves / kParts;
+  static constexpr int kSubs = kKeys / 32;
   static constexpr int kGroups = kKeys / 16;               // of 16 keys, each under one scale
   static constexpr int kTile = kKeys * D;                  // fp16 values of a K or V tile
   static constexpr int kChunks = kKeys * D / 16;           // 16-byte pieces of codes of a K or V tile
   static constexpr int kPasses = (kChunks + kThreads - 1) / kThreads;
+  static constexpr int kScaleWords = 3 * kGroups + 4;
   static constexpr int kMeet = kParts > 1 ? kWaves * 16 * 64 : 0;  // fp32 scores of the waves
-  static constexpr int kLds = 2 * (2 * kTile * 2 + 2 * kGroups * 4) + kMeet * 4;
+  static constexpr int kLds = 2 * (2 * kTile * 2 + kScaleWords * 4) + kMeet * 4;
 };
 
-// What a thread carries of a tile on its way: codes, and one of its scales.
-template <int D>
-struct Staged {
-  u32x4 k[Shape<D>::kPasses], v[Shape<D>::kPasses];
-  float scale;
-};
-
-template <int D, bool HALVES>
-__global__ __launch_bounds__(Shape<D>::kThreads, D <= 128 && !HALVES ? 2 : 1) void tile_kernel(
+// EXACT: sums of weights in fp32, else of the weights as rounded to fp16 (half the instructions; what
+// the values are multiplied with, so that outputs lose nothing, but lse would).
+template <int D, bool HALVES, bool EXACT>
+__global__ __launch_bounds__((Shape<D, HALVES>::kThreads), (Shape<D, HALVES>::kWaves / 4)) void tile_kernel(
     Cache c, Batch b, Attention a, int splits, void *ws, int tiles) {
-  using S = Shape<D>;
+  using S = Shape<D, HALVES>;
   constexpr int kSteps = S::kDims / 16, kDimTiles = S::kDims / 32, kParts = S::kParts;
+  constexpr int kSubs = S::kSubs, kGroups = S::kGroups, kPasses = S::kPasses;
   extern __shared__ __align__(16) char lds[];
   _Float16 *const kt = reinterpret_cast<_Float16 *>(lds);     // [2][kTile]
   _Float16 *const vt = kt + 2 * S::kTile;                     // [2][kTile]
-  float *const scales = reinterpret_cast<float *>(vt + 2 * S::kTile);  // [2][k, v][kGroups]
-  float *const meet = scales + 4 * S::kGroups;                         // [wave][16][64]
-  const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
+  float *const scales = reinterpret_cast<float *>(vt + 2 * S::kTile);  // [2][kScaleWords], see put
+  float *const meet = scales + 2 * S::kScaleWords;                     // [wave][16][64]
+  const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
   const int part_of = wave % kParts, dim0 = part_of * S::kDims;  // this wave's dims
   const int half = lane >> 5, col = lane & 31;
   // late tiles of a sequence have the most keys: they start first
@@ -71,12 +82,13 @@ __global__ __launch_bounds__(Shape<D>::kThreads, D <= 128 && !HALVES ? 2 : 1) vo
   const int pos = row_ok ? q.first + tok : -1;
   const int pos_lo = q.first + wr0 / a.group, pos_hi = wave_ok ? q.first + tok_hi : -1;
 
-  // the keys: tiles [t_begin, t_end) from key0 on
+  // the keys: n tiles from first_key on, counted from 0 below
   const int key0 = a.window ? max(wg_lo - a.window + 1, 0) & ~(S::kKeys - 1) : 0;
   const int key_end = wg_hi + 1;
   const int n_tiles = max(key_end - key0 + S::kKeys - 1, 0) / S::kKeys;
   const int per = (n_tiles + splits - 1) / splits;
-  const int t_begin = split * per, t_end = min(n_tiles, t_begin + per);
+  const int t_begin = split * per, n = min(n_tiles, t_begin + per) - t_begin;
+  const int first_key = key0 + t_begin * S::kKeys;
 
   // query operands: lane (half, col) holds dims 16 i + 8 half + 0 .. 7 of the wave's dims of row col
   h8 qh[kSteps], ql[HALVES ? kSteps : 1];
@@ -107,60 +119,109 @@ __global__ __launch_bounds__(Shape<D>::kThreads, D <= 128 && !HALVES ? 2 : 1) vo
   });
 
   // ---- staging ----
-  // piece ch of a tile's K (or V) codes: group ch / D of 16 keys, piece ch % D of its 16 * D bytes
-  int pages[2][S::kPasses];  // of this thread's pieces, two tiles ahead; -1: none
-  int scale_page[2];
-  const int scale_group = tid % S::kGroups;
-  const bool scale_mine = tid < 2 * S::kGroups, scale_is_v = tid >= S::kGroups;
-  auto look_up = [&](int t, int slot) {
-    const int key = key0 + t * S::kKeys;
-#pragma unroll
-    for (int p = 0; p < S::kPasses; ++p) {
-      const int k16 = key + 16 * ((tid + p * S::kThreads) / D);
-      pages[slot][p] = t < t_end && k16 < key_end ? page_of(c, b, s, k16) : -1;
-    }
-    const int k16 = key + 16 * scale_group;
-    scale_page[slot] = scale_mine && t < t_end && k16 < key_end ? page_of(c, b, s, k16) : -1;
+  // Piece ch of a tile's K (or V) codes: group ch / D of 16 keys, piece ch % D of its 16 * D bytes.
+  // Keys behind the last one take its page, and tiles behind the last are fetched like others: no
+  // row sees them, and nothing branches.
+  const int32_t *const table = b.table + (int64_t)s * b.width;
+  const int in_page = (1 << c.page_log) - 1;
+  const int64_t page_bytes = (int64_t)(c.n_kv << c.page_log) * D, head_bytes = (int64_t)(head << c.page_log) * D;
+  struct Pages {
+    int of[kPasses], of_scale;  // as the table has them
   };
-  auto fetch = [&](int t, int slot, Staged<D> &g) {
-    const int key = key0 + t * S::kKeys;
+  auto look_up = [&](int t) {
+    Pages r;
+    const int key = first_key + t * S::kKeys;
 #pragma unroll
-    for (int p = 0; p < S::kPasses; ++p) {
-      const int ch = tid + p * S::kThreads;
-      g.k[p] = g.v[p] = u32x4{0, 0, 0, 0};
-      if (pages[slot][p] >= 0 && (S::kChunks % S::kThreads == 0 || ch < S::kChunks)) {
-        const int64_t at = code_offset(c, pages[slot][p], head, key + 16 * (ch / D)) + 16 * (ch % D);
-        g.k[p] = *reinterpret_cast<const u32x4 *>(c.k + at);
-        g.v[p] = *reinterpret_cast<const u32x4 *>(c.v + at);
-      }
-    }
-    g.scale = as<float>(0x7fc00000u);  // keys without a page: NaN where a row sees them
-    if (scale_page[slot] >= 0) g.scale = (scale_is_v ? c.vs : c.ks)[scale_offset(c, scale_page[slot], head, key + 16 * scale_group)];
+    for (int p = 0; p < kPasses; ++p) r.of[p] = table[min(key + 16 * ((tid + p * S::kThreads) / D), key_end - 1) >> c.page_log];
+    r.of_scale = table[min(key + 16 * (lane % kGroups), key_end - 1) >> c.page_log];
+    return r;
   };
-  auto put = [&](int buf, const Staged<D> &g) {
-    _Float16 *const kb = kt + buf * S::kTile, *const vb = vt + buf * S::kTile;
+  struct Codes {
+    u32x4 of[kPasses];
+  };
+  auto fetch = [&](const int8_t *codes, int t, const Pages &pages) {
+    Codes r;
+    const int key = first_key + t * S::kKeys;
 #pragma unroll
-    for (int p = 0; p < S::kPasses; ++p) {
+    for (int p = 0; p < kPasses; ++p) {
+      const int ch = min(tid + p * S::kThreads, S::kChunks - 1);
+      const int page = (uint32_t)pages.of[p] < (uint32_t)c.n_pages ? pages.of[p] : 0;  // its scales will be NaN
+      const int at = ((key + 16 * (ch / D)) & in_page) * D + 16 * (ch % D);
+      r.of[p] = *reinterpret_cast<const u32x4 *>(codes + (page * page_bytes + head_bytes) + at);
+    }
+    return r;
+  };
+  struct Scales {
+    float k, v;
+  };
+  auto fetch_scales = [&](int t, const Pages &pages) {  // lane i: of group i % kGroups
+    const bool ok = (uint32_t)pages.of_scale < (uint32_t)c.n_pages;
+    const int64_t at = scale_offset(c, ok ? pages.of_scale : 0, head, first_key + t * S::kKeys + 16 * (lane % kGroups));
+    Scales r{c.ks[at], c.vs[at]};
+    if (!ok) r.k = r.v = as<float>(0x7fc00000u);
+    return r;
+  };
+  auto put_k = [&](int t, const Codes &g) {
+    _Float16 *const kb = kt + (t & 1) * S::kTile;
+#pragma unroll
+    for (int p = 0; p < kPasses; ++p) {
       const int ch = tid + p * S::kThreads, group = ch / D, piece = ch % D;
       if (S::kChunks % S::kThreads != 0 && ch >= S::kChunks) break;
-      // K: 16 dims of one key -> operand (32 keys, 16 dims), halves of 8 dims
+      // 16 dims of one key -> operand (32 keys, 16 dims), halves of 8 dims
       _Float16 *kd = kb + ((group >> 1) * (D / 16) + (piece >> 4)) * 512 + (16 * (group & 1) + (piece & 15)) * 8;
-      *reinterpret_cast<h8 *>(kd) = codes_f16(g.k[p][0], g.k[p][1]);
-      *reinterpret_cast<h8 *>(kd + 256) = codes_f16(g.k[p][2], g.k[p][3]);
-      // V: 4 dims of 4 keys -> operand (32 dims, 16 keys) of this group.  Of the N dims of a wave,
-      // operand row n holds dim 4 (n % (N / 4)) + n / (N / 4), so that the dims that adjacent lanes
-      // write at once are adjacent rows
+      *reinterpret_cast<h8 *>(kd) = codes_f16(g.of[p][0], g.of[p][1]);
+      *reinterpret_cast<h8 *>(kd + 256) = codes_f16(g.of[p][2], g.of[p][3]);
+    }
+  };
+  auto put_v = [&](int t, const Codes &g) {
+    _Float16 *const vb = vt + (t & 1) * S::kTile;
+#pragma unroll
+    for (int p = 0; p < kPasses; ++p) {
+      const int ch = tid + p * S::kThreads, group = ch / D, piece = ch % D;
+      if (S::kChunks % S::kThreads != 0 && ch >= S::kChunks) break;
+      // 4 dims of 4 keys -> operand (32 dims, 16 keys) of this group.  Of the N dims of a wave, operand
+      // row r holds dim 4 (r % (N / 4)) + r / (N / 4), so that the dims that adjacent lanes write at
+      // once are adjacent rows
       const int quad = piece / (D / 4), d4 = piece % (D / 4);
       _Float16 *vd = vb + group * (D / 32) * 512 + (quad & 1) * 256 + (quad >> 1) * 4;
 #pragma unroll
       for (int j = 0; j < 4; ++j) {
-        const int n = d4 / (S::kDims / 4) * S::kDims + j * (S::kDims / 4) + d4 % (S::kDims / 4);
-        *reinterpret_cast<h4 *>(vd + (n >> 5) * 512 + (n & 31) * 8) = codes_f16(g.v[p][j]);
+        const int r = d4 / (S::kDims / 4) * S::kDims + j * (S::kDims / 4) + d4 % (S::kDims / 4);
+        *reinterpret_cast<h4 *>(vd + (r >> 5) * 512 + (r & 31) * 8) = codes_f16(g.of[p][j]);
       }
     }
-    if (scale_mine) scales[(buf * 2 + scale_is_v) * S::kGroups + scale_group] = g.scale;
+  };
+  // Of each group: K's scale; with E the largest exponent of the tile's scales of V, log2(V's / 2^E), which goes
+  // into the weights' exponent, and 2^E / V's, by which a group's sum of weights is multiplied again: an
+  // addition less for each weight than a product.  Of the tile: E, and the least exponent (kNoFold where a
+  // scale is zero, no number, or under 2^-8 of another: weights vanish there that the rows' sums need).
+  auto put_scales = [&](int t, const Scales &g) {
+    if (wave != 0) return;
+    const int i = lane % kGroups;
+    const bool absent = first_key + t * S::kKeys + 16 * i >= key_end, number = g.v > 0.f && g.v < INFINITY;
+    int most = number && !absent ? exponent_of(g.v) : kNoScale;
+    int least = absent ? -kNoFold : number ? most : kNoFold;
+#pragma unroll
+    for (int j = 1; j < kGroups; j <<= 1) {
+      most = max(most, __shfl_xor(most, j));
+      least = min(least, __shfl_xor(least, j));
+    }
+    if (least < most - kFoldBits) least = kNoFold;
+    const float v = absent ? 1.f : ldexp_fast(g.v, -most);
+    float *const sc = scales + (t & 1) * S::kScaleWords;
+    if (lane < kGroups) {
+      sc[lane] = g.k;
+      sc[kGroups + lane] = log2_fast(v);
+      sc[2 * kGroups + lane] = absent ? 0.f : __builtin_amdgcn_rcpf(v);
+    }
+    if (lane == 0) {
+      int *const of_tile = reinterpret_cast<int *>(sc + 3 * kGroups);
+      of_tile[0] = most;
+      of_tile[1] = least;
+    }
   };
 
+  // ---- products ----
   f32x16 o[kDimTiles];
 #pragma unroll
   for (int i = 0; i < kDimTiles; ++i)
@@ -168,125 +229,246 @@ __global__ __launch_bounds__(Shape<D>::kThreads, D <= 128 && !HALVES ? 2 : 1) vo
     for (int j = 0; j < 16; ++j) o[i][j] = 0.f;
   float m = kLowest, l = 0.f;
   int e = kNoScale;
-
-  Staged<D> g;
-  look_up(t_begin, 0);
-  look_up(t_begin + 1, 1);
-  fetch(t_begin, 0, g);
-  if (t_begin < t_end) put(0, g);
-  fetch(t_begin + 1, 1, g);
-  look_up(t_begin + 2, 0);
-  __syncthreads();
-
-  for (int t = t_begin; t < t_end; ++t) {
-    const int buf = (t - t_begin) & 1;
-    if (t + 1 < t_end) {
-      put(buf ^ 1, g);
-      fetch(t + 2, 0, g);
-      look_up(t + 3, 0);
-    }
-    const int tile_key = key0 + t * S::kKeys;
+  auto scale_sums = [&](float f) {
 #pragma unroll
-    for (int sub = 0; sub < S::kKeys / 32; ++sub) {
-      const int key = tile_key + 32 * sub;
-      const bool seen = key <= pos_hi && !(a.window && key + 31 <= pos_lo - a.window);  // by a row of this wave
-      if (kParts == 1 && !seen) continue;
-      const _Float16 *const kb = kt + buf * S::kTile + (sub * (D / 16) + dim0 / 16) * 512 + lane * 8;
-      f32x16 z;
+    for (int i = 0; i < kDimTiles; ++i)
 #pragma unroll
-      for (int j = 0; j < 16; ++j) z[j] = 0.f;
+      for (int j = 0; j < 16; ++j) o[i][j] *= f;
+  };
+  // products of the keys of tile t and this wave's rows (and dims)
+  auto multiply_k = [&](int t, f32x16 (&z)[kSubs]) {
+    const _Float16 *const kb = kt + (t & 1) * S::kTile + dim0 / 16 * 512 + lane * 8;
 #pragma unroll
-      for (int i = 0; i < kSteps; ++i) {
-        const h8 k = *reinterpret_cast<const h8 *>(kb + i * 512);
-        z = mfma32(k, qh[i], z);
-        if constexpr (HALVES) z = mfma32(k, ql[i], z);
+    for (int sub = 0; sub < kSubs; ++sub)
+#pragma unroll
+      for (int j = 0; j < 16; ++j) z[sub][j] = 0.f;
+#pragma unroll
+    for (int i = 0; i < kSteps; ++i)
+#pragma unroll
+      for (int sub = 0; sub < kSubs; ++sub) {
+        const h8 k = *reinterpret_cast<const h8 *>(kb + (sub * (D / 16) + i) * 512);
+        z[sub] = mfma32(k, qh[i], z[sub]);
+        if constexpr (HALVES) z[sub] = mfma32(k, ql[i], z[sub]);
       }
-      if constexpr (kParts > 1) {  // one tile a step, so the barrier behind it also frees this memory
-        static_assert(S::kKeys == 32 && kParts == 2, "");
+  };
+  // two waves' sums over their dims; every wave of the workgroup comes here
+  auto meet_scores = [&](f32x16 (&z)[kSubs]) {
+    if constexpr (kParts > 1) {
+      static_assert(kSubs == 1 && kParts == 2, "memory for 16 scores a lane");
 #pragma unroll
-        for (int j = 0; j < 16; ++j) meet[(wave * 16 + j) * 64 + lane] = z[j];
-        __syncthreads();
-        // both waves add in the same order: their weights are the same bits
+      for (int j = 0; j < 16; ++j) meet[(wave * 16 + j) * 64 + lane] = z[0][j];
+      __syncthreads();
+      // the sum of two is the same in either order: both waves have the same weights
+#pragma unroll
+      for (int j = 0; j < 16; ++j) z[0][j] += meet[((wave ^ 1) * 16 + j) * 64 + lane];
+    }
+  };
+  // weights of tile t times its values
+  auto multiply_v = [&](int t, const h8 (&ph)[kGroups], const h8 (&pl)[kGroups]) {
+    const _Float16 *const vb = vt + (t & 1) * S::kTile + part_of * kDimTiles * 512 + lane * 8;
+#pragma unroll
+    for (int u = 0; u < kGroups; ++u)
+#pragma unroll
+      for (int i = 0; i < kDimTiles; ++i) {
+        const h8 v = *reinterpret_cast<const h8 *>(vb + (u * (D / 32) + i) * 512);
+        o[i] = mfma32(v, ph[u], o[i]);
+        if constexpr (HALVES) o[i] = mfma32(v, pl[u], o[i]);
+      }
+  };
+
+  // A tile's scores on their way to weights: log2 of the weights times V's scale over 2^e, and what
+  // a group's sum of them is multiplied with.
+  float y[kSubs][16], share[kGroups];
+  auto weights = [&](h8 (&ph)[kGroups], h8 (&pl)[kGroups], float &add) {
+    float sum[kGroups];
+#pragma unroll
+    for (int u = 0; u < kGroups; ++u) {
+      float p[8];
+      sum[u] = 0.f;
+#pragma unroll
+      for (int j = 0; j < 8; ++j) {
+        p[j] = exp2_fast(y[u >> 1][8 * (u & 1) + j]);
+        if constexpr (EXACT) sum[u] += p[j];
+        ph[u][j] = (_Float16)p[j];
+        if constexpr (HALVES) pl[u][j] = (_Float16)(p[j] - (float)ph[u][j]);
+      }
+      if constexpr (!EXACT) {
+        const h2 one = {(_Float16)1.f, (_Float16)1.f};
+#pragma unroll
+        for (int j = 0; j < 8; j += 2) sum[u] = __builtin_amdgcn_fdot2(h2{ph[u][j], ph[u][j + 1]}, one, sum[u], false);
+      }
+    }
+    float most = sum[0];
+    add = sum[0] * share[0];
+#pragma unroll
+    for (int u = 1; u < kGroups; ++u) {
+      most += sum[u];
+      add = __builtin_fmaf(sum[u], share[u], add);
+    }
+    return most;
+  };
+  // A row's weights are too large for fp16: its bound moves up to its largest score.
+  auto raise = [&] {
+    float top = y[0][0];
+#pragma unroll
+    for (int sub = 0; sub < kSubs; ++sub)
+#pragma unroll
+      for (int j = 0; j < 16; ++j) top = fmaxf(top, y[sub][j]);
+    top = fmaxf(top, __shfl_xor(top, 32));
+    const float by = fmaxf(top - kBias, 0.f);
+    m += by;
+    const float f = exp2_fast(-by);
+    l *= f;
+    scale_sums(f);
+#pragma unroll
+    for (int sub = 0; sub < kSubs; ++sub)
+#pragma unroll
+      for (int j = 0; j < 16; ++j) y[sub][j] -= by;
+  };
+  auto all_weights = [&](h8 (&ph)[kGroups], h8 (&pl)[kGroups]) {
+    float add;
+    if (__any(weights(ph, pl, add) > kMostSum)) {
+      rare();
+      raise();
+      weights(ph, pl, add);
+    }
+    l += add;
+  };
+  // y of tile t from its products, before the rare cases below
+  float fk[kGroups], lw[kGroups];
+  int e_next, least;
+  auto tile_scales = [&](int t) {
+    const float *const sc = scales + (t & 1) * S::kScaleWords;
+    const int *const of_tile = reinterpret_cast<const int *>(sc + 3 * kGroups);
+    const int most = __builtin_amdgcn_readfirstlane(of_tile[0]);
+    least = __builtin_amdgcn_readfirstlane(of_tile[1]);
+    e_next = max(e, most);
+    const float shift = (float)(most - e_next), back = ldexp_fast(1.f, e_next - most);
+#pragma unroll
+    for (int i = 0; i < kGroups; ++i) {
+      fk[i] = sc[i] * factor;
+      lw[i] = sc[kGroups + i] + shift;
+      share[i] = sc[2 * kGroups + i] * back;
+    }
+  };
+  auto scale_scores = [&](const f32x16 (&z)[kSubs]) {
+    const float mb = m - kBias;
+    float add[kGroups];
+#pragma unroll
+    for (int i = 0; i < kGroups; ++i) add[i] = lw[i] - mb;
+#pragma unroll
+    for (int sub = 0; sub < kSubs; ++sub)
+#pragma unroll
+      for (int j = 0; j < 16; ++j) y[sub][j] = __builtin_fmaf(z[sub][j], fk[2 * sub + (j >> 3)], add[2 * sub + (j >> 3)]);
+  };
+  // What is not in every tile: keys that some row of the wave does not see, a scale of V above all
+  // before, a row's first keys (its bound is not set), scales that do not fold.
+  auto rare_cases = [&](int t, const f32x16 (&z)[kSubs]) {
+    const int key = first_key + t * S::kKeys;
+    const bool ragged = key + S::kKeys - 1 > pos_lo || (a.window && key <= pos_hi - a.window);
+    auto unseen = [&](int sub, int j) {
+      const int at = key + 32 * sub + 8 * (j >> 2) + 4 * half + (j & 3);
+      return at > pos || (a.window && at <= pos - a.window);
+    };
+    if (ragged) {
+      rare();
+#pragma unroll
+      for (int sub = 0; sub < kSubs; ++sub)
+#pragma unroll
+        for (int j = 0; j < 16; ++j) y[sub][j] = unseen(sub, j) ? -INFINITY : y[sub][j];
+      // groups that no row sees may have any scale
+#pragma unroll
+      for (int i = 0; i < kGroups; ++i)
+        if (key + 16 * i > pos_hi || (a.window && key + 16 * i + 15 <= pos_lo - a.window)) share[i] = 0.f;
+    }
+    if (e_next > e) {
+      rare();
+      scale_sums(ldexp_fast(1.f, e - e_next));
+      e = e_next;
+    }
+    const bool unfolded = least < e - kFoldBits;
+    if (unfolded || __any(m == kLowest)) {
+      rare();
+      float top = kLowest;
+#pragma unroll
+      for (int sub = 0; sub < kSubs; ++sub)
 #pragma unroll
         for (int j = 0; j < 16; ++j) {
-          const float x = meet[((wave ^ 1) * 16 + j) * 64 + lane];
-          z[j] = z[j] + x;
+          const float x = __builtin_fmaf(z[sub][j], fk[2 * sub + (j >> 3)], 0.f);
+          y[sub][j] = unseen(sub, j) ? -INFINITY : x;
+          top = fmaxf(top, y[sub][j]);
         }
-        if (!seen) continue;
-      }
-      const float *const sc = scales + buf * 2 * S::kGroups + 2 * sub;
-      const float f0 = sc[0] * factor, f1 = sc[1] * factor;
-      const float v0 = sc[S::kGroups], v1 = sc[S::kGroups + 1];
-      const bool ragged = key + 31 > pos_lo || (a.window && key <= pos_hi - a.window);
-      float y[16];
-      auto weigh = [&](float mb) {  // log2 of the weights under bound mb: scores under 0
+      top = fmaxf(top, __shfl_xor(top, 32));
+      const float was = m;
+      m = fmaxf(m, top);
+      const float f = exp2_fast(was - m);
+      l *= f;
+      scale_sums(f);
+      const float mb = m - kBias;
 #pragma unroll
-        for (int j = 0; j < 16; ++j) y[j] = __builtin_fmaf(z[j], j < 8 ? f0 : f1, -mb);
-        if (ragged) {
+      for (int sub = 0; sub < kSubs; ++sub)
 #pragma unroll
-          for (int j = 0; j < 16; ++j) {
-            const int at = key + 8 * (j >> 2) + 4 * half + (j & 3);
-            if (at > pos || (a.window && at <= pos - a.window)) y[j] = -INFINITY;
-          }
+        for (int j = 0; j < 16; ++j) {
+          const float x = y[sub][j] - mb;
+          if (unfolded) l += exp2_fast(x);
+          y[sub][j] = x == -INFINITY ? x : x + lw[2 * sub + (j >> 3)];
         }
-      };
-      auto largest = [&] {
-        float top = fmaxf(y[0], y[1]);
+      if (unfolded) {
 #pragma unroll
-        for (int j = 2; j < 16; j += 2) top = fmaxf(fmaxf(top, y[j]), y[j + 1]);
-        return top;
-      };
-      weigh(m - kBias);
-      if (__any(largest() > kSlack + kBias)) {
-        weigh(0.f);
-        float top = largest();
-        top = fmaxf(top, __shfl_xor(top, 32));
-        const float was = m;
-        m = fmaxf(m, top);
-        const float f = exp2_fast(was - m);
-        l *= f;
-#pragma unroll
-        for (int i = 0; i < kDimTiles; ++i)
-#pragma unroll
-          for (int j = 0; j < 16; ++j) o[i][j] *= f;
-        // from the rounded scores, as the bound is: scores of 2^28 have no other that is below it
-#pragma unroll
-        for (int j = 0; j < 16; ++j) y[j] -= m - kBias;
+        for (int i = 0; i < kGroups; ++i) share[i] = 0.f;
       }
-      int e2 = kNoScale;
-      if (v0 != 0.f && key <= pos_hi) e2 = exponent_of(v0);
-      if (v1 != 0.f && key + 16 <= pos_hi) e2 = max(e2, exponent_of(v1));
-      e2 = __builtin_amdgcn_readfirstlane(e2);
-      if (e2 > e) {
-        const float f = ldexp_fast(1.f, e - e2);
-        e = e2;
-#pragma unroll
-        for (int i = 0; i < kDimTiles; ++i)
-#pragma unroll
-          for (int j = 0; j < 16; ++j) o[i][j] *= f;
-      }
-      const float w0 = ldexp_fast(v0, -e), w1 = ldexp_fast(v1, -e);
-      h8 ph[2], pl[2];
-#pragma unroll
-      for (int j = 0; j < 16; ++j) {
-        const float p = exp2_fast(y[j]);
-        l += p;
-        float x = p * (j < 8 ? w0 : w1);
-        if (ragged && y[j] == -INFINITY) x = 0.f;  // also where the scale is not finite
-        ph[j >> 3][j & 7] = (_Float16)x;
-        if constexpr (HALVES) pl[j >> 3][j & 7] = (_Float16)(x - (float)ph[j >> 3][j & 7]);
-      }
-      const _Float16 *const vb = vt + buf * S::kTile + (2 * sub * (D / 32) + part_of * kDimTiles) * 512 + lane * 8;
-#pragma unroll
-      for (int u = 0; u < 2; ++u)
-#pragma unroll
-        for (int i = 0; i < kDimTiles; ++i) {
-          const h8 v = *reinterpret_cast<const h8 *>(vb + (u * (D / 32) + i) * 512);
-          o[i] = mfma32(v, ph[u], o[i]);
-          if constexpr (HALVES) o[i] = mfma32(v, pl[u], o[i]);
-        }
+    }
+  };
+
+  if (n > 0) {
+    Codes k_next, v_next;
+    Scales s_next;
+    Pages pk, pv;
+    {
+      const Pages p0 = look_up(0), p1 = look_up(1);
+      pv = look_up(2);
+      pk = look_up(3);
+      const Codes k0 = fetch(c.k, 0, p0), k1 = fetch(c.k, 1, p1), v0 = fetch(c.v, 0, p0);
+      const Scales s0 = fetch_scales(0, p0), s1 = fetch_scales(1, p1);
+      v_next = fetch(c.v, 1, p1);
+      k_next = fetch(c.k, 2, pv);
+      s_next = fetch_scales(2, pv);
+      put_k(0, k0);
+      put_scales(0, s0);
+      put_k(1, k1);
+      put_scales(1, s1);
+      put_v(0, v0);
     }
     __syncthreads();
+    f32x16 z[kSubs];
+    multiply_k(0, z);
+    meet_scores(z);
+    tile_scales(0);
+    scale_scores(z);
+    rare_cases(0, z);
+    __syncthreads();  // K's first buffer is free
+    h8 ph[kGroups], pl[kGroups];
+    for (int t = 0; t + 1 < n; ++t) {
+      // K of t + 1, V of t and the scales of t + 1 are in LDS; K of t + 2, V of t + 1 in registers
+      multiply_k(t + 1, z);
+      all_weights(ph, pl);
+      meet_scores(z);
+      put_k(t + 2, k_next);
+      put_v(t + 1, v_next);
+      put_scales(t + 2, s_next);
+      k_next = fetch(c.k, t + 3, pk);
+      v_next = fetch(c.v, t + 2, pv);
+      s_next = fetch_scales(t + 3, pk);
+      pv = pk;
+      pk = look_up(t + 4);
+      multiply_v(t, ph, pl);
+      tile_scales(t + 1);
+      scale_scores(z);
+      rare_cases(t + 1, z);
+      __syncthreads();
+    }
+    all_weights(ph, pl);
+    multiply_v(n - 1, ph, pl);
   }
 
   l += __shfl_xor(l, 32);
@@ -307,8 +489,8 @@ __global__ __launch_bounds__(Shape<D>::kThreads, D <= 128 && !HALVES ? 2 : 1) vo
       float v[4];
 #pragma unroll
       for (int j = 0; j < 4; ++j) {
-        const int n = j * (S::kDims / 4) + 8 * i + k, r = n & 31;  // (operand row of the lanes' first half)
-        v[j] = l == 0.f ? 0.f : o[n >> 5][4 * (r >> 3) + (r & 3)] * fin.factor;
+        const int d = j * (S::kDims / 4) + 8 * i + k, r = d & 31;  // (operand row of the lanes' first half)
+        v[j] = l == 0.f ? 0.f : o[d >> 5][4 * (r >> 3) + (r & 3)] * fin.factor;
       }
       const int dim = dim0 + 4 * (8 * i + 4 * half + k);
       if (splits > 1)
@@ -318,20 +500,29 @@ __global__ __launch_bounds__(Shape<D>::kThreads, D <= 128 && !HALVES ? 2 : 1) vo
     }
 }
 
-template <int D, bool HALVES>
-hipError_t launch_dim(const Cache &c, const Batch &b, const Attention &a, int splits, void *ws, hipStream_t s) {
-  using S = Shape<D>;
-  static const hipError_t ready = hipFuncSetAttribute(reinterpret_cast<const void *>(tile_kernel<D, HALVES>),
+template <int D, bool HALVES, bool EXACT>
+hipError_t launch_kernel(const Cache &c, const Batch &b, const Attention &a, int splits, void *ws, hipStream_t s) {
+  using S = Shape<D, HALVES>;
+  static const hipError_t ready = hipFuncSetAttribute(reinterpret_cast<const void *>(tile_kernel<D, HALVES, EXACT>),
                                                       hipFuncAttributeMaxDynamicSharedMemorySize, S::kLds);
   if (ready != hipSuccess) return ready;
   const int tiles = (int)((int64_t)b.n_tok * a.group / S::kRows + b.n_seq);
-  tile_kernel<D, HALVES><<<dim3((uint32_t)tiles * c.n_kv, (uint32_t)splits), S::kThreads, S::kLds, s>>>(c, b, a, splits, ws, tiles);
+  tile_kernel<D, HALVES, EXACT><<<dim3((uint32_t)tiles * c.n_kv, (uint32_t)splits), S::kThreads, S::kLds, s>>>(c, b, a, splits, ws, tiles);
   return hipGetLastError();
+}
+
+template <int D, bool HALVES>
+hipError_t launch_dim(const Cache &c, const Batch &b, const Attention &a, int splits, void *ws, hipStream_t s) {
+  if (HALVES || a.lse) return launch_kernel<D, HALVES, true>(c, b, a, splits, ws, s);
+  return launch_kernel<D, HALVES, HALVES>(c, b, a, splits, ws, s);
 }
 
 }  // namespace
 
-int tile_rows(int d) { return d > 256 ? Shape<512>::kRows : Shape<256>::kRows; }
+int tile_rows(int d, bool halves) {
+  if (d > 256) return Shape<512, false>::kRows;
+  return d > 128 || halves ? Shape<256, false>::kRows : Shape<128, false>::kRows;
+}
 
 hipError_t launch_tile(const Cache &c, const Batch &b, const Attention &a, int splits, void *ws, hipStream_t s) {
   const bool halves = a.q.type == kF32 || a.out_type == kF32;
