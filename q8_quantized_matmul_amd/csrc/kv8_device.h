@@ -130,6 +130,43 @@ __device__ __forceinline__ void load_values(const void *p, int64_t at, bool wide
   }
 }
 
+// Eight adjacent values as they lie in memory.
+template <int TYPE>
+struct Eight {
+  u32x4 raw[TYPE == kF32 ? 2 : 1];
+  __device__ __forceinline__ void load(const void *p, int64_t at, bool wide) {
+    if constexpr (TYPE == kF32) {
+      const uint32_t *x = static_cast<const uint32_t *>(p) + at;
+      if (wide) {
+        raw[0] = reinterpret_cast<const u32x4 *>(x)[0];
+        raw[1] = reinterpret_cast<const u32x4 *>(x)[1];
+      } else {
+#pragma unroll
+        for (int j = 0; j < 8; ++j) raw[j >> 2][j & 3] = x[j];
+      }
+    } else {
+      const uint16_t *x = static_cast<const uint16_t *>(p) + at;
+      if (wide) {
+        raw[0] = *reinterpret_cast<const u32x4 *>(x);
+      } else {
+#pragma unroll
+        for (int j = 0; j < 4; ++j) raw[0][j] = x[2 * j] | (uint32_t)x[2 * j + 1] << 16;
+      }
+    }
+  }
+  __device__ __forceinline__ float get(int j) const {
+    if constexpr (TYPE == kF32) return as<float>(raw[j >> 2][j & 3]);
+    const uint32_t bits = raw[0][j >> 1] >> (16 * (j & 1));
+    return TYPE == kBF16 ? as<float>(bits << 16) : (float)as<_Float16>((uint16_t)bits);
+  }
+  __device__ __forceinline__ uint32_t amax_bits() const {
+    uint32_t m = 0;
+#pragma unroll
+    for (int j = 0; j < 8; ++j) m = max(m, as<uint32_t>(get(j)) & 0x7fffffffu);
+    return m;
+  }
+};
+
 // bf16 and fp16 bits, rounded to nearest even.
 __device__ __forceinline__ uint32_t bf16_bits(float v) { return as<uint16_t>((__bf16)v); }
 __device__ __forceinline__ uint32_t f16_bits(float v) { return as<uint16_t>((_Float16)v); }

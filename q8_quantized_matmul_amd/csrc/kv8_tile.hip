@@ -29,10 +29,16 @@ constexpr float kMostSum = 0x1p15f;
 // In a branch that is hardly ever taken: what follows is not to be computed ahead of it.
 __device__ __forceinline__ void rare() { asm volatile(""); }
 
+// A lane's neighbour's value (0xb1), or that of the lane two on (0x4e), within four lanes.
+template <int CTRL>
+__device__ __forceinline__ int swapped(int v) {
+  return __builtin_amdgcn_mov_dpp(v, CTRL, 0xf, 0xf, false);
+}
+
 template <int D, bool HALVES>
 struct Shape {
   static constexpr int kKeys = D <= 128 ? 64 : 32;         // of a tile
-  static constexpr int kWaves = D <= 128 && !HALVES ? 8 : 4;
+  static constexpr int kWaves = D == 128 && !HALVES ? 8 : 4;
   static constexpr int kParts = D > 256 ? 2 : 1;           // waves that share 32 rows
   static constexpr int kDims = D / kParts;                 // dims of a wave
   static constexpr int kThreads = 64 * kWaves;
@@ -47,9 +53,7 @@ struct Shape {
   static constexpr int kLds = 2 * (2 * kTile * 2 + kScaleWords * 4) + kMeet * 4;
 };
 
-// EXACT: sums of weights in fp32, else of the weights as rounded to fp16 (half the instructions; what
-// the values are multiplied with, so that outputs lose nothing, but lse would).
-template <int D, bool HALVES, bool EXACT>
+template <int D, bool HALVES>
 __global__ __launch_bounds__((Shape<D, HALVES>::kThreads), (Shape<D, HALVES>::kWaves / 4)) void tile_kernel(
     Cache c, Batch b, Attention a, int splits, void *ws, int tiles) {
   using S = Shape<D, HALVES>;
@@ -93,30 +97,36 @@ __global__ __launch_bounds__((Shape<D, HALVES>::kThreads), (Shape<D, HALVES>::kW
   // query operands: lane (half, col) holds dims 16 i + 8 half + 0 .. 7 of the wave's dims of row col
   h8 qh[kSteps], ql[HALVES ? kSteps : 1];
   const int64_t q_at = (int64_t)(q.row0 + tok) * a.q.token_stride + (int64_t)q_head * a.q.head_stride + 8 * half;
-  const float factor = by_type(a.q.type, [&](auto type) {
-    uint32_t amax = 0;
+  float factor = 0.f;
+  auto load_queries = [&] {
+    factor = by_type(a.q.type, [&](auto type) {
+      Eight<type.value> x[kSteps];
 #pragma unroll
-    for (int i = 0; i < D / 16; ++i) {
-      float v[8];
-      load_values<type.value, 8>(a.q.p, q_at + 16 * i, a.q.wide, v);
+      for (int i = 0; i < kSteps; ++i) x[i].load(a.q.p, q_at + dim0 + 16 * i, a.q.wide);
+      uint32_t amax = 0;
 #pragma unroll
-      for (int j = 0; j < 8; ++j) amax = max(amax, as<uint32_t>(v[j]) & 0x7fffffffu);
-    }
-    amax = max(amax, (uint32_t)__shfl_xor((int)amax, 32));
-    const RowScale rs(as<float>(amax), a.scale);
+      for (int i = 0; i < kSteps; ++i) amax = max(amax, x[i].amax_bits());
+      if constexpr (kParts > 1) {
 #pragma unroll
-    for (int i = 0; i < kSteps; ++i) {
-      float v[8];
-      load_values<type.value, 8>(a.q.p, q_at + dim0 + 16 * i, a.q.wide, v);
-#pragma unroll
-      for (int j = 0; j < 8; ++j) {
-        const float x = ldexp_fast(v[j], -rs.e);
-        qh[i][j] = (_Float16)x;
-        if constexpr (HALVES) ql[i][j] = (_Float16)(x - (float)qh[i][j]);
+        for (int i = 0; i < kSteps; ++i) {
+          Eight<type.value> other;
+          other.load(a.q.p, q_at + (S::kDims - dim0) + 16 * i, a.q.wide);
+          amax = max(amax, other.amax_bits());
+        }
       }
-    }
-    return rs.factor;
-  });
+      amax = max(amax, (uint32_t)__shfl_xor((int)amax, 32));
+      const RowScale rs(as<float>(amax), a.scale);
+#pragma unroll
+      for (int i = 0; i < kSteps; ++i)
+#pragma unroll
+        for (int j = 0; j < 8; ++j) {
+          const float v = ldexp_fast(x[i].get(j), -rs.e);
+          qh[i][j] = (_Float16)v;
+          if constexpr (HALVES) ql[i][j] = (_Float16)(v - (float)qh[i][j]);
+        }
+      return rs.factor;
+    });
+  };
 
   // ---- staging ----
   // Piece ch of a tile's K (or V) codes: group ch / D of 16 keys, piece ch % D of its 16 * D bytes.
@@ -202,9 +212,9 @@ __global__ __launch_bounds__((Shape<D, HALVES>::kThreads), (Shape<D, HALVES>::kW
     int most = number && !absent ? exponent_of(g.v) : kNoScale;
     int least = absent ? -kNoFold : number ? most : kNoFold;
 #pragma unroll
-    for (int j = 1; j < kGroups; j <<= 1) {
-      most = max(most, __shfl_xor(most, j));
-      least = min(least, __shfl_xor(least, j));
+    for (int j = 1; j < kGroups; j <<= 1) {  // among four lanes, or two
+      most = max(most, j == 1 ? swapped<0xb1>(most) : swapped<0x4e>(most));
+      least = min(least, j == 1 ? swapped<0xb1>(least) : swapped<0x4e>(least));
     }
     if (least < most - kFoldBits) least = kNoFold;
     const float v = absent ? 1.f : ldexp_fast(g.v, -most);
@@ -288,14 +298,9 @@ __global__ __launch_bounds__((Shape<D, HALVES>::kThreads), (Shape<D, HALVES>::kW
 #pragma unroll
       for (int j = 0; j < 8; ++j) {
         p[j] = exp2_fast(y[u >> 1][8 * (u & 1) + j]);
-        if constexpr (EXACT) sum[u] += p[j];
+        sum[u] += p[j];
         ph[u][j] = (_Float16)p[j];
         if constexpr (HALVES) pl[u][j] = (_Float16)(p[j] - (float)ph[u][j]);
-      }
-      if constexpr (!EXACT) {
-        const h2 one = {(_Float16)1.f, (_Float16)1.f};
-#pragma unroll
-        for (int j = 0; j < 8; j += 2) sum[u] = __builtin_amdgcn_fdot2(h2{ph[u][j], ph[u][j + 1]}, one, sum[u], false);
       }
     }
     float most = sum[0];
@@ -424,6 +429,7 @@ __global__ __launch_bounds__((Shape<D, HALVES>::kThreads), (Shape<D, HALVES>::kW
     Codes k_next, v_next;
     Scales s_next;
     Pages pk, pv;
+    if constexpr (D == 64) load_queries();  // (beside the fetches its scalar registers do not fit)
     {
       const Pages p0 = look_up(0), p1 = look_up(1);
       pv = look_up(2);
@@ -433,6 +439,7 @@ __global__ __launch_bounds__((Shape<D, HALVES>::kThreads), (Shape<D, HALVES>::kW
       v_next = fetch(c.v, 1, p1);
       k_next = fetch(c.k, 2, pv);
       s_next = fetch_scales(2, pv);
+      if constexpr (D != 64) load_queries();
       put_k(0, k0);
       put_scales(0, s0);
       put_k(1, k1);
@@ -500,28 +507,22 @@ __global__ __launch_bounds__((Shape<D, HALVES>::kThreads), (Shape<D, HALVES>::kW
     }
 }
 
-template <int D, bool HALVES, bool EXACT>
-hipError_t launch_kernel(const Cache &c, const Batch &b, const Attention &a, int splits, void *ws, hipStream_t s) {
+template <int D, bool HALVES>
+hipError_t launch_dim(const Cache &c, const Batch &b, const Attention &a, int splits, void *ws, hipStream_t s) {
   using S = Shape<D, HALVES>;
-  static const hipError_t ready = hipFuncSetAttribute(reinterpret_cast<const void *>(tile_kernel<D, HALVES, EXACT>),
+  static const hipError_t ready = hipFuncSetAttribute(reinterpret_cast<const void *>(tile_kernel<D, HALVES>),
                                                       hipFuncAttributeMaxDynamicSharedMemorySize, S::kLds);
   if (ready != hipSuccess) return ready;
   const int tiles = (int)((int64_t)b.n_tok * a.group / S::kRows + b.n_seq);
-  tile_kernel<D, HALVES, EXACT><<<dim3((uint32_t)tiles * c.n_kv, (uint32_t)splits), S::kThreads, S::kLds, s>>>(c, b, a, splits, ws, tiles);
+  tile_kernel<D, HALVES><<<dim3((uint32_t)tiles * c.n_kv, (uint32_t)splits), S::kThreads, S::kLds, s>>>(c, b, a, splits, ws, tiles);
   return hipGetLastError();
-}
-
-template <int D, bool HALVES>
-hipError_t launch_dim(const Cache &c, const Batch &b, const Attention &a, int splits, void *ws, hipStream_t s) {
-  if (HALVES || a.lse) return launch_kernel<D, HALVES, true>(c, b, a, splits, ws, s);
-  return launch_kernel<D, HALVES, HALVES>(c, b, a, splits, ws, s);
 }
 
 }  // namespace
 
 int tile_rows(int d, bool halves) {
   if (d > 256) return Shape<512, false>::kRows;
-  return d > 128 || halves ? Shape<256, false>::kRows : Shape<128, false>::kRows;
+  return d == 128 && !halves ? Shape<128, false>::kRows : Shape<256, false>::kRows;
 }
 
 hipError_t launch_tile(const Cache &c, const Batch &b, const Attention &a, int splits, void *ws, hipStream_t s) {
