@@ -85,22 +85,68 @@ size_t partial_bytes(const Cache &c, const Batch &b, int n_q, int splits) {
   return splits > 1 ? (size_t)splits * b.n_tok * n_q * (c.d + 1) * sizeof(float) : 0;
 }
 
-// The tiled kernel for more than 16 rows a sequence and key/value head, but for heads of 512
-// in two halves, whose operands do not fit its registers.
-// Splits: workgroups for each of the 256 compute units, none with less than 128 keys.
-Plan attention_plan(const Cache &c, const Batch &b, int n_q, bool halves, size_t ws_bytes) {
+// Which kernel, and how many splits: the least of the estimated times.  Measured, in us:
+//   stream: a workgroup takes `alone` for 16 rows and 128 keys where it has a compute unit to itself, and a unit
+//     gives one every `shared` where it has several;
+//   tiled: a unit takes `tile` for `keys` keys of all its rows, `at_once` workgroups beside each other.
+// Both take some us before the first key and behind the last, the join of splits some more, and its traffic.
+// What the estimates decide, measured (us, stream / tiled): heads of 128, 8 of them, groups of 4: 256 tokens
+// 9 / 18; 2 x 1000 tokens 90 / 41; 40 sequences of 32 tokens over 2000 keys 117 / 195; 8192 tokens
+// 1368 / 610.  Heads of 512, 64 on one, 2 x 300 tokens over 1000 keys 322 / 240; 12 single tokens over up
+// to 6000 keys 56 / 80.  Splits of one sequence of 2000 keys, 1 / 4 / 16: 20 / 12 / 10; of 131072 keys, 16 / 64:
+// 82 / 48; of 64 sequences of up to 8192, 1 / 4: 133 / 137.
+struct Cost {
+  float alone, shared, tile;
+  int keys, at_once;
+};
+Cost cost_of(int d, bool halves) {
+  const float more = halves ? 1.2f : 1.f;
+  switch (d) {
+    case 64: return {0.9f * more, 0.5f * more, 2.2f * more, 64, 2};
+    case 128: return {1.2f * more, 0.75f * more, 2.4f * more, 64, 1};
+    case 192: return {1.6f * more, 1.1f * more, 2.2f * more, 32, 1};
+    case 256: return {2.0f * more, 1.55f * more, 2.6f * more, 32, 1};
+    default: return {3.0f * more, 3.0f * more, 2.7f * more, 32, 1};
+  }
+}
+
+Plan attention_plan(const Cache &c, const Batch &b, int n_q, int window, bool halves, size_t ws_bytes) {
+  constexpr float kUnits = 256.f, kEnds = 5.f, kTileEnds = 10.f, kJoin = 4.f, kJoinBytes = 4e6f;  // bytes a us
+  const Cost cost = cost_of(c.d, halves);
   const int group = n_q / c.n_kv;
   const int64_t most_rows = (int64_t)b.max_new * group;
-  const bool tiled = most_rows > 16 && !(halves && c.d > 256);
-  const int rows = tiled ? tile_rows(c.d, halves) : 16;
-  const int64_t tiles = most_rows > rows ? (int64_t)b.n_tok * group / rows + b.n_seq : b.n_seq;
-  const int64_t units = tiles * c.n_kv;
-  int64_t splits = (512 + units - 1) / units;
-  const int64_t most = (b.max_len + 127) / 128;
-  if (splits > most) splits = most;
-  if (splits > 256) splits = 256;
-  while (splits > 1 && partial_bytes(c, b, n_q, (int)splits) > ws_bytes) --splits;
-  return {tiled, splits < 1 ? 1 : (int)splits};
+  auto workgroups = [&](int rows) {
+    return (float)((most_rows > rows ? (int64_t)b.n_tok * group / rows + b.n_seq : b.n_seq) * c.n_kv);
+  };
+  // keys of the longest row tile, and of a mean one: rows of a prompt see half of it
+  float longest = (float)b.max_len;
+  if (window && (float)window + (float)b.max_new < longest) longest = (float)window + (float)b.max_new;
+  const bool prompt = 2.f * (float)b.max_new > longest;
+  const float mean = prompt ? longest - 0.5f * (float)b.max_new : longest;
+
+  Plan best{false, 1};
+  float least = INFINITY;
+  const float streams = workgroups(16);
+  const bool many = (int64_t)b.n_tok * n_q > 1 << 20;  // more than the join is launched for
+  const int most = many || b.max_len < 256 ? 1 : b.max_len / 128 < 256 ? b.max_len / 128 : 256;
+  for (int splits = 1; splits <= most; splits += splits < 8 ? 1 : splits / 4) {
+    const float bytes = (float)partial_bytes(c, b, n_q, splits);
+    if (bytes > (float)ws_bytes) break;
+    const float rounds = prompt ? fmaxf(1.f, streams * splits / kUnits) : ceilf(streams * splits / kUnits);
+    const float t = mean / (128.f * splits) * fmaxf(cost.alone, cost.shared * rounds) + kEnds * fmaxf(1.f, rounds / 4.f) +
+                    (splits > 1 ? kJoin + 2.f * bytes / kJoinBytes : 0.f);
+    if (t < least) {
+      least = t;
+      best.splits = splits;
+    }
+  }
+  if (!(halves && c.d > 256)) {  // its operands do not fit the registers
+    const float each = workgroups(tile_rows(c.d, halves)) / (kUnits * cost.at_once);
+    const float rounds = prompt ? fmaxf(1.f, each) : ceilf(each);
+    const float t = fmaxf(longest / cost.keys * cost.tile + kTileEnds, rounds * (mean / cost.keys * cost.tile + kTileEnds));
+    if (t < least) best = {true, 1};
+  }
+  return best;
 }
 
 }  // namespace kv
@@ -146,7 +192,7 @@ size_t kv8_attention_workspace_bytes(const kv8_cache *cache, const kv8_batch *ba
     return 0;
   size_t most = 0;
   for (bool halves : {false, true}) {
-    const kv::Plan p = kv::attention_plan(c, b, n_q, halves, SIZE_MAX);
+    const kv::Plan p = kv::attention_plan(c, b, n_q, 0, halves, SIZE_MAX);
     const size_t bytes = kv::partial_bytes(c, b, n_q, p.splits);
     if (bytes > most) most = bytes;
   }
@@ -172,7 +218,7 @@ int kv8_attention(const kv8_cache *cache, const kv8_batch *batch, const kv8_atte
   if (!aligned(x.out, 16) || !aligned(x.sinks, 4) || !aligned(x.lse, 4) || !aligned(workspace, 16)) return Q8_0_EALIGN;
   if ((st = q8::check_device()) != Q8_0_OK) return st;
   const bool halves = x.q_type == KV8_F32 || x.out_type == KV8_F32;
-  const kv::Plan p = kv::attention_plan(c, b, x.n_q, halves, workspace ? workspace_bytes : 0);
+  const kv::Plan p = kv::attention_plan(c, b, x.n_q, x.window, halves, workspace ? workspace_bytes : 0);
   hipError_t e = p.tiled ? kv::launch_tile(c, b, a, p.splits, workspace, stream)
                          : kv::launch_stream(c, b, a, p.splits, workspace, stream);
   if (e == hipSuccess && p.splits > 1) e = kv::launch_join(c, b, a, p.splits, workspace, stream);

@@ -50,7 +50,7 @@ struct Plan {
   bool tiled;  // kv8_tile.hip, or kv8_stream.hip
   int splits;
 };
-Plan attention_plan(const Cache &c, const Batch &b, int n_q, bool halves, size_t ws_bytes);
+Plan attention_plan(const Cache &c, const Batch &b, int n_q, int window, bool halves, size_t ws_bytes);
 size_t partial_bytes(const Cache &c, const Batch &b, int n_q, int splits);
 
 // kv8_tile.hip; tile_rows: query rows of a workgroup

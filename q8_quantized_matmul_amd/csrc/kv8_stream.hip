@@ -251,40 +251,84 @@ __global__ __launch_bounds__(256) void stream_kernel(Cache c, Batch b, Attention
   }
 }
 
-// out[row] = sum over splits of out_s * exp2(lse2_s) / (their sum, and the sink's); splits in order.
-// A thread takes 4 dims of a row.
+
+// out[row] = sum over splits of out_s * exp2(lse2_s) / (their sum, and the sink's).  A thread takes 4 dims.  Up to
+// kFewSplits a workgroup takes as many rows as fit, a thread all splits of its row; above, one row, of which a thread
+// has every n-th split (what bounds it is latency: a row's loads are on their way together), and the n
+// sums are added in order.
+constexpr int kMostSplits = 256, kFewSplits = 8;
 __global__ __launch_bounds__(256) void join_kernel(Cache c, Batch b, Attention a, int splits, const void *ws) {
+  __shared__ float weight[kMostSplits], wave_top[4], wave_sum[4];
+  __shared__ f32x4 sums[256];
   const Partials part(const_cast<void *>(ws), b, c, a.n_q, splits);
-  const int lanes = c.d / 4;
-  const int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x;
-  const int64_t row = i / lanes;
-  const int at = (int)(i - row * lanes) * 4;
+  const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
+  const int lanes = c.d / 4, groups = 256 / lanes, group = tid / lanes, at = tid % lanes * 4;
+  const bool few = splits <= kFewSplits;
+  const int64_t row = few ? (int64_t)blockIdx.x * groups + group : blockIdx.x;
   const int tok = (int)(row / a.n_q), head = (int)(row - (int64_t)tok * a.n_q);
-  if (row >= part.rows || tok < start_of(b, 0) || tok >= (b.starts ? start_of(b, b.n_seq) : b.n_seq)) return;
-  float top = -INFINITY;
-  bool nan = false;
-  for (int s = 0; s < splits; ++s) {
-    const float z = part.lse2[s * part.rows + row];
-    top = fmaxf(top, z);
-    nan |= z != z;
-  }
-  float sum = 0.f, v[4] = {0.f, 0.f, 0.f, 0.f};
-  if (top > -INFINITY || nan) {
-    for (int s = 0; s < splits; ++s) {
-      const float z = part.lse2[s * part.rows + row];
-      if (z == -INFINITY) continue;
-      const float f = exp2_fast(z - top);
-      const f32x4 x = *reinterpret_cast<const f32x4 *>(part.out + (s * part.rows + row) * c.d + at);
-      sum += f;
+  bool mine = group < groups && row < part.rows && tok >= start_of(b, 0) && tok < (b.starts ? start_of(b, b.n_seq) : b.n_seq);
+  if (!few && !__any(mine)) return;  // one row: the same for all
+  const float *const x = part.out + row * c.d + at;
+  const int64_t stride = part.rows * c.d;
+  float top = -INFINITY, sum = 0.f;
+  f32x4 v = {0.f, 0.f, 0.f, 0.f};
+  if (few) {
+    if (!mine) return;
+    float z[kFewSplits];
+    f32x4 y[kFewSplits];
 #pragma unroll
-      for (int j = 0; j < 4; ++j) v[j] += x[j] * f;
+    for (int s = 0; s < kFewSplits; ++s) {
+      z[s] = s < splits ? part.lse2[s * part.rows + row] : -INFINITY;
+      if (s < splits) y[s] = *reinterpret_cast<const f32x4 *>(x + s * stride);
+      top = fmaxf(top, z[s]);
+    }
+#pragma unroll
+    for (int s = 0; s < kFewSplits; ++s) {
+      const float w = z[s] == -INFINITY ? 0.f : exp2_fast(z[s] - top);
+      sum += w;
+#pragma unroll
+      for (int j = 0; j < 4; ++j) v[j] += w == 0.f ? 0.f : y[s][j] * w;  // (nothing was written where it is 0)
+    }
+  } else {
+    const float z = tid < splits ? part.lse2[tid * part.rows + row] : -INFINITY;
+    top = z;
+#pragma unroll
+    for (int i = 1; i < 64; i <<= 1) top = fmaxf(top, __shfl_xor(top, i));
+    if (lane == 0) wave_top[wave] = top;
+    __syncthreads();
+    top = fmaxf(fmaxf(wave_top[0], wave_top[1]), fmaxf(wave_top[2], wave_top[3]));
+    const float w = z == -INFINITY ? 0.f : exp2_fast(z - top);
+    weight[tid] = w;
+    sum = w;
+#pragma unroll
+    for (int i = 1; i < 64; i <<= 1) sum += __shfl_xor(sum, i);
+    if (lane == 0) wave_sum[wave] = sum;
+    __syncthreads();
+    sum = (wave_sum[0] + wave_sum[1]) + (wave_sum[2] + wave_sum[3]);
+    if (group < groups) {
+#pragma unroll 8
+      for (int s = group; s < splits; s += groups) {
+        const float f = weight[s];
+        const f32x4 y = *reinterpret_cast<const f32x4 *>(x + s * stride);
+#pragma unroll
+        for (int j = 0; j < 4; ++j) v[j] += f == 0.f ? 0.f : y[j] * f;
+      }
+    }
+    sums[tid] = v;
+    __syncthreads();
+    if (group != 0) return;
+    for (int i = 1; i < groups; ++i) {
+      const f32x4 y = sums[i * lanes + tid];
+#pragma unroll
+      for (int j = 0; j < 4; ++j) v[j] += y[j];
     }
   }
   // weights relative to the largest: a sum of them is a sum of kBias more
-  Finish fin(top + kBias, sum, 0, a.sinks ? a.sinks[head] * kLog2e : -INFINITY);
+  const Finish fin(top + kBias, sum, 0, a.sinks ? a.sinks[head] * kLog2e : -INFINITY);
+  float out[4];
 #pragma unroll
-  for (int j = 0; j < 4; ++j) v[j] = sum == 0.f ? 0.f : v[j] * fin.factor;
-  store_row<4>(a.out, a.out_type, row * c.d + at, v);
+  for (int j = 0; j < 4; ++j) out[j] = sum == 0.f ? 0.f : v[j] * fin.factor;
+  store_row<4>(a.out, a.out_type, row * c.d + at, out);
   if (at == 0 && a.lse) a.lse[row] = fin.lse2 * kLn2;
 }
 
@@ -312,8 +356,8 @@ hipError_t launch_stream(const Cache &c, const Batch &b, const Attention &a, int
 }
 
 hipError_t launch_join(const Cache &c, const Batch &b, const Attention &a, int splits, const void *ws, hipStream_t s) {
-  const int64_t threads = (int64_t)b.n_tok * a.n_q * (c.d / 4);
-  join_kernel<<<dim3((uint32_t)((threads + 255) / 256)), 256, 0, s>>>(c, b, a, splits, ws);
+  const uint32_t rows = (uint32_t)b.n_tok * a.n_q, groups = 256 / (c.d / 4);
+  join_kernel<<<dim3(splits <= kFewSplits ? (rows + groups - 1) / groups : rows), 256, 0, s>>>(c, b, a, splits, ws);
   return hipGetLastError();
 }
 

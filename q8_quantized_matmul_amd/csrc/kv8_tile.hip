@@ -447,6 +447,16 @@ __global__ __launch_bounds__((Shape<D, HALVES>::kThreads), (Shape<D, HALVES>::kW
       put_v(0, v0);
     }
     __syncthreads();
+    auto stage = [&](int t) {  // beside tile t's values: the next tiles to LDS, others on their way
+      put_k(t + 2, k_next);
+      put_v(t + 1, v_next);
+      put_scales(t + 2, s_next);
+      k_next = fetch(c.k, t + 3, pk);
+      v_next = fetch(c.v, t + 2, pv);
+      s_next = fetch_scales(t + 3, pk);
+      pv = pk;
+      pk = look_up(t + 4);
+    };
     f32x16 z[kSubs];
     multiply_k(0, z);
     meet_scores(z);
@@ -460,14 +470,7 @@ __global__ __launch_bounds__((Shape<D, HALVES>::kThreads), (Shape<D, HALVES>::kW
       multiply_k(t + 1, z);
       all_weights(ph, pl);
       meet_scores(z);
-      put_k(t + 2, k_next);
-      put_v(t + 1, v_next);
-      put_scales(t + 2, s_next);
-      k_next = fetch(c.k, t + 3, pk);
-      v_next = fetch(c.v, t + 2, pv);
-      s_next = fetch_scales(t + 3, pk);
-      pv = pk;
-      pk = look_up(t + 4);
+      stage(t);
       multiply_v(t, ph, pl);
       tile_scales(t + 1);
       scale_scores(z);
