@@ -128,12 +128,14 @@ Plan attention_plan(const Cache &c, const Batch &b, int n_q, int window, bool ha
   float least = INFINITY;
   const float streams = workgroups(16);
   const bool many = (int64_t)b.n_tok * n_q > 1 << 20;  // more than the join is launched for
-  const int most = many || b.max_len < 256 ? 1 : b.max_len / 128 < 256 ? b.max_len / 128 : 256;
-  for (int splits = 1; splits <= most; splits += splits < 8 ? 1 : splits / 4) {
+  const int units = (b.max_len + 127) / 128;  // of 128 keys, a step of a workgroup's four waves
+  for (int each = units; each >= 1; each -= each > 8 ? (each + 7) / 8 : 1) {
+    const int splits = (units + each - 1) / each;
+    if (splits > 256 || (many && splits > 1)) break;
     const float bytes = (float)partial_bytes(c, b, n_q, splits);
-    if (bytes > (float)ws_bytes) break;
+    if (bytes > (float)ws_bytes) continue;
     const float rounds = prompt ? fmaxf(1.f, streams * splits / kUnits) : ceilf(streams * splits / kUnits);
-    const float t = mean / (128.f * splits) * fmaxf(cost.alone, cost.shared * rounds) + kEnds * fmaxf(1.f, rounds / 4.f) +
+    const float t = fminf((float)each, ceilf(mean / 128.f)) * fmaxf(cost.alone, cost.shared * rounds) + kEnds * fmaxf(1.f, rounds / 4.f) +
                     (splits > 1 ? kJoin + 2.f * bytes / kJoinBytes : 0.f);
     if (t < least) {
       least = t;

@@ -48,7 +48,7 @@ __global__ __launch_bounds__(256) void stream_kernel(Cache c, Batch b, Attention
   const int key0 = a.window ? max(pos_lo - a.window + 1, 0) & ~(kStep - 1) : 0;
   const int key_end = pos_hi + 1;
   const int steps = max(key_end - key0 + kStep - 1, 0) / kStep;
-  const int per = (steps + splits - 1) / splits;
+  const int per = ((steps + splits - 1) / splits + kWaves - 1) / kWaves * kWaves;  // whole turns of the waves
   const int st_end = min(steps, (split + 1) * per);
   const int st_begin = split * per + wave;
 

@@ -23,9 +23,11 @@ struct Share {
         dim0(is_k ? lane >> 4 << 4 : (lane & 15) << 2) {}
 };
 
-// x / s to the nearest integer, ties to even, by the exact quotient: x * (1 / s) is within
-// 3 * 2^-24 * 127.5 < 2^-15 of it, so only quotients nearer than 2^-12 to a tie need more.  The
-// difference x - n * s is exact in 64 bits, and so is its comparison with s / 2.
+// x / s to the nearest integer, ties to even, by the exact quotient.  What the callers round in fp32 is off by
+// at most 127.5 * 2^-23 < 2^-16 (a reciprocal or ratio and a product, each rounded once), so only quotients
+// nearer than 2^-15 to a tie come here: 6 % of the waves have one among 1024 values (with a margin of 2^-12,
+// half of them: 16384 tokens of 8 heads of 128 took 39 us).  The difference x - n * s is exact in 64 bits,
+// and so is its comparison with s / 2.
 __device__ __forceinline__ float settle(float n, double x, double s) {
   const double r2 = 2.0 * __builtin_fma(-(double)n, s, x);
   if (r2 > s || (r2 == s && ((int)n & 1))) n += 1.f;
@@ -34,7 +36,7 @@ __device__ __forceinline__ float settle(float n, double x, double s) {
 }
 
 constexpr float kMagic = 12582912.f;  // 1.5 * 2^23: x + kMagic rounds x to an integer, in the low bits
-constexpr float kNearTie = 0.5f - 0x1p-12f;
+constexpr float kNearTie = 0.5f - 0x1p-15f;
 
 // Codes of 16 values under scale s (finite, not negative), inv = 1 / s.
 __device__ __forceinline__ u32x4 encode16(const float (&x)[16], float s, float inv) {
@@ -66,37 +68,58 @@ __device__ __forceinline__ u32x4 encode16(const float (&x)[16], float s, float i
   return w;
 }
 
-// Four codes under scale s0 as codes under the larger s1, nearest even of the exact quotient.
-__device__ __forceinline__ uint32_t requantize4(uint32_t codes, float s0, float s1) {
+// 16 codes under scale s0 as codes under the larger s1, nearest even of the exact quotient; those of
+// `older` bytes only.
+__device__ __forceinline__ u32x4 requantize16(u32x4 codes, float s0, float s1, uint32_t older) {
   const float ratio = s0 / s1;
-  uint32_t w = 0;
+  float n[16], far = 0.f;
 #pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    const float q = (float)(int8_t)(codes >> (8 * i));
-    const float n = settle(__builtin_rintf(q * ratio), (double)q * (double)s0, s1);
-    w |= ((uint32_t)(int)n & 255u) << (8 * i);
+  for (int i = 0; i < 16; ++i) {
+    const float x = (float)(int8_t)(codes[i >> 2] >> (8 * (i & 3))) * ratio;
+    n[i] = __builtin_rintf(x);
+    far = fmaxf(far, __builtin_fabsf(x - n[i]));
   }
-  return w;
-}
-
-__device__ __forceinline__ uint32_t wave_max(uint32_t v) {
+  if (!(far < kNearTie)) {
 #pragma unroll
-  for (int i = 1; i < 64; i <<= 1) v = max(v, (uint32_t)__shfl_xor((int)v, i));
-  return v;
+    for (int i = 0; i < 16; ++i)
+      n[i] = settle(n[i], (double)(int8_t)(codes[i >> 2] >> (8 * (i & 3))) * (double)s0, s1);
+  }
+#pragma unroll
+  for (int j = 0; j < 4; ++j) {
+    uint32_t w = 0;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) w |= ((uint32_t)(int)n[4 * j + i] & 255u) << (8 * i);
+    codes[j] = (w & older) | (codes[j] & ~older);
+  }
+  return codes;
 }
 
-// blockIdx.x: a slot of the batch's blocks; blockIdx.y: kUnits of the 2 * n_kv arrays of heads
-// (all of K, then all of V).
+template <int CTRL>
+__device__ __forceinline__ uint32_t max_with(uint32_t v) {
+  return max(v, (uint32_t)__builtin_amdgcn_mov_dpp((int)v, CTRL, 0xf, 0xf, false));
+}
+// The largest of the wave's values, without a detour through LDS.
+__device__ __forceinline__ uint32_t wave_max(uint32_t v) {
+  v = max_with<0xb1>(v);   // lanes 1 apart
+  v = max_with<0x4e>(v);   // 2
+  v = max_with<0x141>(v);  // the other four of eight
+  v = max_with<0x140>(v);  // the other eight of sixteen
+  auto a = __builtin_amdgcn_permlane16_swap(v, v, false, false);
+  v = max(a[0], a[1]);
+  auto b = __builtin_amdgcn_permlane32_swap(v, v, false, false);
+  return max(b[0], b[1]);
+}
+
+// blockIdx.x: a slot of the batch's blocks; blockIdx.y: kUnits of the 2 * n_kv arrays of heads (all of K,
+// then all of V).  (Several turns of kUnits in a workgroup, which then looks its block up once for them, took
+// 37.5 to 39 us for 16384 tokens of 8 heads of 128 instead of 36.5.)
 template <int TYPE, int D, int BLOCK_WAVES>
 __global__ __launch_bounds__(kWriteThreads(BLOCK_WAVES)) void write_kernel(Cache c, Batch b, Rows kr, Rows vr) {
   constexpr int kWaves = kWriteThreads(BLOCK_WAVES) / 64, kUnits = kWaves / BLOCK_WAVES;
   constexpr int kBlock = 16 * BLOCK_WAVES, kPasses = D / 64;
   __shared__ uint32_t wave_amax[kWaves];
-  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+  const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int part = wave % BLOCK_WAVES;
-  const int unit = blockIdx.y * kUnits + wave / BLOCK_WAVES;
-  const bool is_k = unit < c.n_kv;
-  const int head = is_k ? unit : unit - c.n_kv;
 
   // which sequence, which of its blocks
   int s = blockIdx.x, nth = 0;
@@ -108,54 +131,74 @@ __global__ __launch_bounds__(kWriteThreads(BLOCK_WAVES)) void write_kernel(Cache
   const Span q = span_of(b, c, s);
   const int base = (max(q.first, 0) >> c.block_log << c.block_log) + nth * kBlock;
   const int t0 = max(q.first - base, 0), t1 = min(q.len - base, kBlock);  // new tokens of the block
-  int page = -1;
-  if (unit < 2 * c.n_kv && t0 < t1) page = page_of(c, b, s, base);
-  const bool live = page >= 0;
+  if (t0 >= t1) return;
+  const int page = page_of(c, b, s, base);
+  if (page < 0) return;
 
-  // this lane's tokens of the block: at[i] = first + i
+  const int mine = blockIdx.y * kUnits + wave / BLOCK_WAVES, unit = min(mine, 2 * c.n_kv - 1);
+  const bool idle = mine != unit;  // only passes the barrier
+  const bool is_k = unit < c.n_kv;
+  const int head = is_k ? unit : unit - c.n_kv;
+  // this lane's tokens of the block: first + i
   const Share sh(is_k, lane);
   const int first = 16 * part + sh.token0;
+  // bytes of a lane's 16 that are new, or older ones
+  uint32_t fresh = 0, older = 0;
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const int t = first + (is_k ? 0 : i);
+    if (!idle && t >= t0 && t < t1) fresh |= 255u << (8 * i);
+    if (!idle && t < t0) older |= 255u << (8 * i);
+  }
   const Rows &r = is_k ? kr : vr;
   const int64_t row = ((int64_t)q.row0 + base + first - q.first) * r.token_stride + (int64_t)head * r.head_stride + sh.dim0;
-  float x[kPasses][16];
-  uint32_t amax = 0;
+  float *const scale = (is_k ? c.ks : c.vs) + scale_offset(c, page, head, base);
+  int8_t *const codes = (is_k ? c.k : c.v) + code_offset(c, page, head, base + 16 * part);
+  // K [dims / 16][token][16]: a chunk of 16 dims is 256 bytes, a wave's pass 1024.
+  // V [token / 4][dim][4]: four tokens are 4 * D bytes.
+  const int at0 = is_k ? 16 * lane : sh.token0 * D + 4 * sh.dim0, at_step = is_k ? 1024 : 256;
+
+  // all loads first: rows, and where the block or this lane's bytes hold others, what they hold
   float s0 = 0.f;
-  float *scale = (is_k ? c.ks : c.vs) + (live ? scale_offset(c, page, head, base) : 0);
-  if (live) {
-    if (t0 > 0) s0 = *scale;
-    if (is_k) {
-      const bool mine = first >= t0 && first < t1;
+  if (t0 > 0) s0 = *scale;
+  u32x4 was[kPasses];
+  if (fresh != 0xffffffffu && (fresh | older)) {
 #pragma unroll
-      for (int p = 0; p < kPasses; ++p) {
-        if (mine) {
-          load_values<TYPE, 16>(r.p, row + 64 * p, r.wide, x[p]);
-        } else {
+    for (int p = 0; p < kPasses; ++p) was[p] = *reinterpret_cast<const u32x4 *>(codes + at0 + p * at_step);
+  }
+  float x[kPasses][16];
+  if (is_k) {
 #pragma unroll
-          for (int i = 0; i < 16; ++i) x[p][i] = 0.f;
-        }
-      }
-    } else {
+    for (int p = 0; p < kPasses; ++p) {
+      if (fresh) {
+        load_values<TYPE, 16>(r.p, row + 64 * p, r.wide, x[p]);
+      } else {
 #pragma unroll
-      for (int p = 0; p < kPasses; ++p) {
-        float t[4][4];
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          if (first + i >= t0 && first + i < t1) {
-            load_values<TYPE, 4>(r.p, row + i * r.token_stride + 64 * p, r.wide, t[i]);
-          } else {
-#pragma unroll
-            for (int j = 0; j < 4; ++j) t[i][j] = 0.f;
-          }
-        }
-#pragma unroll
-        for (int i = 0; i < 16; ++i) x[p][i] = t[i & 3][i >> 2];  // [dim][token], as V's codes lie
+        for (int i = 0; i < 16; ++i) x[p][i] = 0.f;
       }
     }
+  } else {
 #pragma unroll
-    for (int p = 0; p < kPasses; ++p)
+    for (int p = 0; p < kPasses; ++p) {
+      float t[4][4];
 #pragma unroll
-      for (int i = 0; i < 16; ++i) amax = max(amax, as<uint32_t>(x[p][i]) & 0x7fffffffu);
+      for (int i = 0; i < 4; ++i) {
+        if (fresh >> (8 * i) & 1) {
+          load_values<TYPE, 4>(r.p, row + i * r.token_stride + 64 * p, r.wide, t[i]);
+        } else {
+#pragma unroll
+          for (int j = 0; j < 4; ++j) t[i][j] = 0.f;
+        }
+      }
+#pragma unroll
+      for (int i = 0; i < 16; ++i) x[p][i] = t[i & 3][i >> 2];  // [dim][token], as V's codes lie
+    }
   }
+  uint32_t amax = 0;
+#pragma unroll
+  for (int p = 0; p < kPasses; ++p)
+#pragma unroll
+    for (int i = 0; i < 16; ++i) amax = max(amax, as<uint32_t>(x[p][i]) & 0x7fffffffu);
   amax = wave_max(amax);
   if constexpr (BLOCK_WAVES > 1) {
     if (lane == 0) wave_amax[wave] = amax;
@@ -163,45 +206,27 @@ __global__ __launch_bounds__(kWriteThreads(BLOCK_WAVES)) void write_kernel(Cache
 #pragma unroll
     for (int i = 0; i < BLOCK_WAVES; ++i) amax = max(amax, wave_amax[wave - part + i]);
   }
-  if (!live) return;
 
   float s1 = as<float>(amax) / 127.f;  // IEEE division
   if (t0 > 0 && s0 > s1) s1 = s0;
   const bool bad = amax >= 0x7f800000u || (t0 > 0 && s0 != s0);
   if (bad) s1 = as<float>(0x7fc00000u);
-  const bool grown = t0 > 0 && s1 > s0;
-  if (part == 0 && lane == 0) *scale = s1;
+  if (!(t0 > 0 && s1 > s0)) older = 0;  // the scale did not grow
+  if (!idle && part == 0 && lane == 0) *scale = s1;
+  if ((fresh | older) == 0) return;
 
   const float inv = 1.f / s1;
-  int8_t *codes = (is_k ? c.k : c.v) + code_offset(c, page, head, base + 16 * part);
-  // bytes of a lane's 16 that are new, or older ones to be rounded to the new scale
-  uint32_t fresh = 0, older = 0;
-#pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    const int t = first + (is_k ? 0 : i);
-    if (t >= t0 && t < t1) fresh |= 255u << (8 * i);
-    if (t < t0) older |= 255u << (8 * i);
-  }
-  if (!grown) older = 0;
-  if ((fresh | older) == 0) return;
 #pragma unroll
   for (int p = 0; p < kPasses; ++p) {
-    // K [dims / 16][token][16]: a chunk of 16 dims is 256 bytes, a wave's pass 1024.
-    // V [token / 4][dim][4]: four tokens are 4 * D bytes.
-    const int at = is_k ? 1024 * p + 16 * lane : sh.token0 * D + 4 * (64 * p + sh.dim0);
-    u32x4 *dst = reinterpret_cast<u32x4 *>(codes + at);
     u32x4 w = {0, 0, 0, 0};
     if (!bad) w = encode16(x[p], s1, inv);
     if (fresh != 0xffffffffu) {
-      const u32x4 was = *dst;
+      u32x4 old = was[p];
+      if (older) old = requantize16(old, s0, s1, older);
 #pragma unroll
-      for (int j = 0; j < 4; ++j) {
-        uint32_t old = was[j];
-        if (older) old = (requantize4(old, s0, s1) & older) | (old & ~older);
-        w[j] = (w[j] & fresh) | (old & ~fresh);
-      }
+      for (int j = 0; j < 4; ++j) w[j] = (w[j] & fresh) | (old[j] & ~fresh);
     }
-    *dst = w;
+    *reinterpret_cast<u32x4 *>(codes + at0 + p * at_step) = w;
   }
 }
 
