@@ -42,7 +42,7 @@ enum { KV8_F32 = 0, KV8_BF16 = 1, KV8_F16 = 2 };
 /* A pool of pages.  Codes must be 16-byte aligned, scales 4-byte aligned. */
 typedef struct kv8_cache {
     void *k_codes, *v_codes;
-    float *k_scales, *v_scales;
+    float *k_scales, *v_scales; /* not negative, as kv8_write makes them             */
     int64_t n_pages;    /* 0 .. 2^31 - 1                                            */
     int32_t n_kv;       /* key/value heads, 1 .. 4096                               */
     int32_t head_dim;   /* 64, 128, 192, 256 or 512                                 */
@@ -63,8 +63,8 @@ typedef struct kv8_batch {
     const int32_t *starts;      /* int32 [n_seq + 1], ascending from 0; NULL: one row each */
     int64_t n_seq;              /* 0 .. 2^20                                         */
     int64_t n_tok;              /* rows of the token arrays, 0 .. 2^24; n_seq where starts is NULL */
-    int64_t table_width;        /* pages of a table row; table_width * page_size < 2^31 */
-    int64_t max_new;            /* no sequence has more rows than this (1 where starts is NULL) */
+    int64_t table_width;        /* pages of a table row; table_width * page_size <= 2^30 */
+    int64_t max_new;            /* no sequence may have more rows than this (1 where starts is NULL) */
     int64_t max_len;            /* no lens[s] is above this: work is spread by it; 0: unknown */
 } kv8_batch;
 
@@ -141,6 +141,23 @@ size_t kv8_attention_workspace_bytes(const kv8_cache *cache, const kv8_batch *ba
  * Q8_0_EINVAL; misaligned pointers -> Q8_0_EALIGN. */
 int kv8_attention(const kv8_cache *cache, const kv8_batch *batch, const kv8_attention_args *args,
                   void *workspace, size_t workspace_bytes, hipStream_t stream);
+
+/* Kernel variants (for kv8_attention_debug; 0 lets the library choose). */
+enum {
+    KV8_KERNEL_AUTO = 0,
+    KV8_KERNEL_STREAM = 1, /* 16 query rows a workgroup, codes straight from memory        */
+    KV8_KERNEL_TILED = 2   /* 64 to 256 query rows a workgroup, codes through LDS as fp16;
+                              not for heads of 512 where out_type or q_type is KV8_F32     */
+};
+
+/* Test hook: kv8_attention by the given kernel with `splits` splits over the keys (0 or 1:
+ * none, up to 256; their workspace is splits * n_tok * n_q * (head_dim + 1) * 4 bytes).  With
+ * KV8_KERNEL_AUTO splits must be 0.
+ * Errors as kv8_attention; a kernel, or splits of more than 2^20 rows (n_tok * n_q), that
+ * do not exist -> Q8_0_EINVAL; workspace too small -> Q8_0_EWORKSPACE. */
+int kv8_attention_debug(const kv8_cache *cache, const kv8_batch *batch, const kv8_attention_args *args,
+                        void *workspace, size_t workspace_bytes, int32_t kernel, int32_t splits,
+                        hipStream_t stream);
 
 #ifdef __cplusplus
 }

@@ -383,6 +383,7 @@ from .mxfp4 import (MOE_SIGMOID, MOE_SOFTMAX, MOE_SQRT_SOFTPLUS, MXFP4_BF16,  # 
                     mxfp4_moe_layer_workspace_bytes, mxfp4_quantize)
 
 # The 8-bit key/value cache (include/kv8.h).
-from .kv8 import (KV8_BF16, KV8_F16, KV8_F32, Kv8Batch, Kv8Cache, kv8_attention,  # noqa: E402
+from .kv8 import (KV8_BF16, KV8_F16, KV8_F32, KV8_KERNEL_AUTO, KV8_KERNEL_STREAM,  # noqa: E402
+                  KV8_KERNEL_TILED, Kv8Batch, Kv8Cache, kv8_attention, kv8_attention_debug,
                   kv8_attention_workspace, kv8_attention_workspace_bytes, kv8_cache, kv8_read,
                   kv8_write)

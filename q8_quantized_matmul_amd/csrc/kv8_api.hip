@@ -25,6 +25,7 @@ int log_of(int64_t v, int64_t lo, int64_t hi) {
   return n;
 }
 
+constexpr int64_t kMaxLen = 1 << 30;  // positions, and the tiles fetched ahead of them, in 32 bits
 constexpr int64_t kMaxSeq = 1 << 20, kMaxTok = 1 << 24, kMaxStride = int64_t{1} << 40;
 // A launch has fewer than 2^32 threads: attention makes a workgroup of 256 for 16 rows and head.
 constexpr int64_t kMaxRows = int64_t{1} << 27, kMaxSeqHeads = int64_t{1} << 22;
@@ -44,7 +45,7 @@ int read_cache(const kv8_cache *c, kv::Cache *out) {
 
 int read_batch(const kv8_batch *b, const kv::Cache &c, kv::Batch *out) {
   if (!b || b->n_seq < 0 || b->n_seq > kMaxSeq || b->n_tok < 0 || b->n_tok > kMaxTok || b->table_width < 0 ||
-      b->table_width > (INT32_MAX >> c.page_log) || b->max_new < 0 || b->max_len < 0 || b->n_seq * c.n_kv > kMaxSeqHeads)
+      b->table_width > (kMaxLen >> c.page_log) || b->max_new < 0 || b->max_len < 0 || b->n_seq * c.n_kv > kMaxSeqHeads)
     return Q8_0_EINVAL;
   if (!b->starts && b->n_tok != b->n_seq) return Q8_0_EINVAL;
   const int64_t room = b->table_width << c.page_log;
@@ -122,12 +123,12 @@ Plan attention_plan(const Cache &c, const Batch &b, int n_q, int window, bool ha
   float longest = (float)b.max_len;
   if (window && (float)window + (float)b.max_new < longest) longest = (float)window + (float)b.max_new;
   const bool prompt = 2.f * (float)b.max_new > longest;
-  const float mean = prompt ? longest - 0.5f * (float)b.max_new : longest;
+  const float mean = prompt ? longest - 0.5f * fminf((float)b.max_new, longest) : longest;  // max_new may be any bound
 
   Plan best{false, 1};
   float least = INFINITY;
   const float streams = workgroups(16);
-  const bool many = (int64_t)b.n_tok * n_q > 1 << 20;  // more than the join is launched for
+  const bool many = (int64_t)b.n_tok * n_q > kMaxJoinRows;
   const int units = (b.max_len + 127) / 128;  // of 128 keys, a step of a workgroup's four waves
   for (int each = units; each >= 1; each -= each > 8 ? (each + 7) / 8 : 1) {
     const int splits = (units + each - 1) / each;
@@ -152,6 +153,46 @@ Plan attention_plan(const Cache &c, const Batch &b, int n_q, int window, bool ha
 }
 
 }  // namespace kv
+
+namespace {
+
+// kernel: KV8_KERNEL_AUTO, or the one to run with `splits` splits (0: one).
+int run_attention(const kv8_cache *cache, const kv8_batch *batch, const kv8_attention_args *args, void *workspace,
+                  size_t workspace_bytes, int32_t kernel, int32_t splits, hipStream_t stream) {
+  kv::Cache c;
+  kv::Batch b;
+  int st = read_cache(cache, &c);
+  if (st == Q8_0_OK) st = read_batch(batch, c, &b);
+  if (st != Q8_0_OK || !args) return Q8_0_EINVAL;
+  const kv8_attention_args &x = *args;
+  if (x.n_q < 1 || x.n_q > kMaxHeads || x.n_q % c.n_kv != 0 || x.window < 0 || !isfinite(x.scale) ||
+      !type_ok(x.out_type) || !type_ok(x.q_type) || (int64_t)b.n_tok * x.n_q > kMaxRows)
+    return Q8_0_EINVAL;
+  const bool halves = x.q_type == KV8_F32 || x.out_type == KV8_F32;
+  if (kernel < KV8_KERNEL_AUTO || kernel > KV8_KERNEL_TILED || splits < 0 || splits > 256 ||
+      (kernel == KV8_KERNEL_AUTO && splits != 0) || (kernel == KV8_KERNEL_TILED && halves && c.d > 256) ||
+      (splits > 1 && (int64_t)b.n_tok * x.n_q > kv::kMaxJoinRows))
+    return Q8_0_EINVAL;
+  if (nothing_to_do(b)) return Q8_0_OK;
+  kv::Attention a{x.out, {}, x.out_type, x.n_q, x.n_q / c.n_kv, x.window, x.scale, x.sinks, x.lse};
+  if ((st = check_pointers(c, b)) != Q8_0_OK || (st = read_rows(x.q, x.q_token_stride, x.q_head_stride, x.q_type, &a.q)) != Q8_0_OK)
+    return st;
+  if (!x.out) return Q8_0_EINVAL;
+  if (!aligned(x.out, 16) || !aligned(x.sinks, 4) || !aligned(x.lse, 4) || !aligned(workspace, 16)) return Q8_0_EALIGN;
+  if (!workspace) workspace_bytes = 0;
+  kv::Plan p{kernel == KV8_KERNEL_TILED, splits > 1 ? splits : 1};
+  if (kernel == KV8_KERNEL_AUTO)
+    p = kv::attention_plan(c, b, x.n_q, x.window, halves, workspace_bytes);
+  else if (kv::partial_bytes(c, b, x.n_q, p.splits) > workspace_bytes)
+    return Q8_0_EWORKSPACE;
+  if ((st = q8::check_device()) != Q8_0_OK) return st;
+  hipError_t e = p.tiled ? kv::launch_tile(c, b, a, p.splits, workspace, stream)
+                         : kv::launch_stream(c, b, a, p.splits, workspace, stream);
+  if (e == hipSuccess && p.splits > 1) e = kv::launch_join(c, b, a, p.splits, workspace, stream);
+  return status_of(e);
+}
+
+}  // namespace
 
 extern "C" {
 
@@ -203,28 +244,13 @@ size_t kv8_attention_workspace_bytes(const kv8_cache *cache, const kv8_batch *ba
 
 int kv8_attention(const kv8_cache *cache, const kv8_batch *batch, const kv8_attention_args *args,
                   void *workspace, size_t workspace_bytes, hipStream_t stream) {
-  kv::Cache c;
-  kv::Batch b;
-  int st = read_cache(cache, &c);
-  if (st == Q8_0_OK) st = read_batch(batch, c, &b);
-  if (st != Q8_0_OK || !args) return Q8_0_EINVAL;
-  const kv8_attention_args &x = *args;
-  if (x.n_q < 1 || x.n_q > kMaxHeads || x.n_q % c.n_kv != 0 || x.window < 0 || !isfinite(x.scale) ||
-      !type_ok(x.out_type) || !type_ok(x.q_type) || (int64_t)b.n_tok * x.n_q > kMaxRows)
-    return Q8_0_EINVAL;
-  if (nothing_to_do(b)) return Q8_0_OK;
-  kv::Attention a{x.out, {}, x.out_type, x.n_q, x.n_q / c.n_kv, x.window, x.scale, x.sinks, x.lse};
-  if ((st = check_pointers(c, b)) != Q8_0_OK || (st = read_rows(x.q, x.q_token_stride, x.q_head_stride, x.q_type, &a.q)) != Q8_0_OK)
-    return st;
-  if (!x.out) return Q8_0_EINVAL;
-  if (!aligned(x.out, 16) || !aligned(x.sinks, 4) || !aligned(x.lse, 4) || !aligned(workspace, 16)) return Q8_0_EALIGN;
-  if ((st = q8::check_device()) != Q8_0_OK) return st;
-  const bool halves = x.q_type == KV8_F32 || x.out_type == KV8_F32;
-  const kv::Plan p = kv::attention_plan(c, b, x.n_q, x.window, halves, workspace ? workspace_bytes : 0);
-  hipError_t e = p.tiled ? kv::launch_tile(c, b, a, p.splits, workspace, stream)
-                         : kv::launch_stream(c, b, a, p.splits, workspace, stream);
-  if (e == hipSuccess && p.splits > 1) e = kv::launch_join(c, b, a, p.splits, workspace, stream);
-  return status_of(e);
+  return run_attention(cache, batch, args, workspace, workspace_bytes, KV8_KERNEL_AUTO, 0, stream);
+}
+
+int kv8_attention_debug(const kv8_cache *cache, const kv8_batch *batch, const kv8_attention_args *args,
+                        void *workspace, size_t workspace_bytes, int32_t kernel, int32_t splits,
+                        hipStream_t stream) {
+  return run_attention(cache, batch, args, workspace, workspace_bytes, kernel, splits, stream);
 }
 
 }  // extern "C"

@@ -50,6 +50,7 @@ struct Plan {
   bool tiled;  // kv8_tile.hip, or kv8_stream.hip
   int splits;
 };
+constexpr int64_t kMaxJoinRows = 1 << 20;  // rows that the join of splits is launched for
 Plan attention_plan(const Cache &c, const Batch &b, int n_q, int window, bool halves, size_t ws_bytes);
 size_t partial_bytes(const Cache &c, const Batch &b, int n_q, int splits);
 

@@ -18,6 +18,7 @@ from . import _i32, _i64, _lib, _sz, _vp
 from .mxfp4 import _calls, _device, _ptr, _run, _scratch, _shape, _type
 
 KV8_F32, KV8_BF16, KV8_F16 = 0, 1, 2
+KV8_KERNEL_AUTO, KV8_KERNEL_STREAM, KV8_KERNEL_TILED = 0, 1, 2
 _I32_MAX = 2 ** 31 - 1
 
 
@@ -46,6 +47,7 @@ _sig = {
     "kv8_read": ([_vp, _vp, _vp, _vp, _i32, _vp], ctypes.c_int),
     "kv8_attention_workspace_bytes": ([_vp, _vp, _i32], _sz),
     "kv8_attention": ([_vp, _vp, _vp, _vp, _sz, _vp], ctypes.c_int),
+    "kv8_attention_debug": ([_vp, _vp, _vp, _vp, _sz, _i32, _i32, _vp], ctypes.c_int),
 }
 for _name, (_args, _res) in _sig.items():
     _fn = getattr(_lib, _name)
@@ -218,6 +220,25 @@ def kv8_attention(cache: Kv8Cache, batch: Kv8Batch, q: torch.Tensor, scale: floa
     among them, as q's type, out_dtype or out's type.  scale: by default 1 / sqrt(head_dim); window:
     keys that a row sees (0: all); sinks: float32 [n_q], a score per head that has no value;
     lse: float32 [n_tok][n_q], receives the log of each row's sum."""
+    return _attend(cache, batch, q, scale, window, sinks, out, out_dtype, lse, workspace)
+
+
+def kv8_attention_debug(cache: Kv8Cache, batch: Kv8Batch, q: torch.Tensor, kernel: int,
+                        splits: int = 0, scale: float = None, window: int = 0,
+                        sinks: torch.Tensor = None, out: torch.Tensor = None,
+                        out_dtype: torch.dtype = None, lse: torch.Tensor = None,
+                        workspace: torch.Tensor = None) -> torch.Tensor:
+    """Test hook: kv8_attention by the given kernel (KV8_KERNEL_*) with that many splits."""
+    if workspace is None:
+        rows = batch.n_tok * (q.shape[1] if q.dim() > 1 else 0)
+        need = splits * rows * (cache.head_dim + 1) * 4 if splits > 1 else 0
+        workspace = torch.empty(need, dtype=torch.uint8, device=cache.device)
+    return _attend(cache, batch, q, scale, window, sinks, out, out_dtype, lse, workspace,
+                   "kv8_attention_debug", kernel, splits)
+
+
+def _attend(cache, batch, q, scale, window, sinks, out, out_dtype, lse, workspace,
+            call="kv8_attention", *choice):
     device = _same_device(cache, batch)
     d, n_tok, n_kv = cache.head_dim, batch.n_tok, cache.n_kv
     qp, qt, qh = _rows(q, "q", n_tok, 0, d, device, q.dtype)
@@ -244,5 +265,5 @@ def kv8_attention(cache: Kv8Cache, batch: Kv8Batch, q: torch.Tensor, scale: floa
                                   if workspace is None else 0, device)
     args = _AttentionArgs(op, qp, qt, qh, _type(out_dtype, "out"), _type(q.dtype, "q"), n_q, window,
                           1.0 / math.sqrt(d) if scale is None else scale, sinks, lse)
-    _run("kv8_attention", device, cache._ref, batch._ref, ctypes.byref(args), ws, ws_bytes)
+    _run(call, device, cache._ref, batch._ref, ctypes.byref(args), ws, ws_bytes, *choice)
     return out

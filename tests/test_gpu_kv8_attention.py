@@ -17,45 +17,59 @@ SIZES = {
 }
 
 
-def run(c, q, **kw):
+def run(c, q, kernel=0, **kw):
     lse = torch.full((c.n_tok, q.shape[1]), 5.0, device="cuda")
-    out = c.q8.kv8_attention(c.cache, kw.pop("batch", c.batch), q, lse=lse, **kw)
+    batch = kw.pop("batch", c.batch)
+    if kernel:
+        out = c.q8.kv8_attention_debug(c.cache, batch, q, kernel, lse=lse, **kw)
+    else:
+        out = c.q8.kv8_attention(c.cache, batch, q, lse=lse, **kw)
     torch.cuda.synchronize()
     return out, lse
 
 
+# the two kernels, whatever the sizes would choose
+both = pytest.mark.parametrize("kernel", [1, 2])
+
+
+@both
 @pytest.mark.parametrize("dtype", list(DTYPES))
 @pytest.mark.parametrize("d,hq,hkv", [(64, 6, 3), (128, 4, 2), (192, 2, 2), (256, 8, 1), (512, 5, 1)])
 @pytest.mark.parametrize("sizes", list(SIZES))
-def test_attention(sizes, d, hq, hkv, dtype):
-    say("attention", sizes, d, hq, hkv, dtype)
+def test_attention(sizes, d, hq, hkv, dtype, kernel):
+    say("attention", sizes, d, hq, hkv, dtype, kernel)
+    if kernel == 2 and d == 512 and dtype == "fp32":
+        pytest.skip("the tiled kernel has no such variant")
     c = Case(SIZES[sizes], hkv, d, seed=d + hq, stale=np.nan, one_row=sizes in ("one", "decode")).upload()
     q, q64 = c.rows(hq, DTYPES[dtype], spread=1.5)
-    out, lse = run(c, q)
+    out, lse = run(c, q, kernel)
     assert out.dtype == q.dtype
     say("worst", c.check_attention(q, q64, out, lse))
 
 
+@both
 @pytest.mark.parametrize("group", [1, 3, 5, 16, 17, 32, 64])
-def test_groups(group):
+def test_groups(group, kernel):
     c = Case([(1, 70), (2, 35), (1, 5)], 2, 64, seed=group).upload()
     q, q64 = c.rows(2 * group, torch.bfloat16)
-    out, lse = run(c, q)
+    out, lse = run(c, q, kernel)
     c.check_attention(q, q64, out, lse)
 
 
+@both
 @pytest.mark.parametrize("page,block", [(16, 16), (32, 32), (256, 16), (128, 128), (1024, 64)])
 @pytest.mark.parametrize("dtype", ["bf16", "fp32"])
-def test_pages_and_blocks(page, block, dtype):
+def test_pages_and_blocks(page, block, dtype, kernel):
     c = Case([(1, 500), (90, 210), (1, 129), (17, 17)], 2, 64, page, block, seed=page, stale=np.inf).upload()
     q, q64 = c.rows(4, DTYPES[dtype])
-    out, lse = run(c, q)
+    out, lse = run(c, q, kernel)
     c.check_attention(q, q64, out, lse)
 
 
+@both
 @pytest.mark.parametrize("window", [1, 2, 31, 32, 33, 64, 100, 1000])
 @pytest.mark.parametrize("sizes", ["decode", "prompt"])
-def test_windows(window, sizes):
+def test_windows(window, sizes, kernel):
     c = Case(SIZES[sizes], 2, 64, 16, seed=window, stale=np.nan).upload()
     # what no window reaches must not matter: NaN scales there
     for s, (n, m) in enumerate(c.sizes):
@@ -65,27 +79,29 @@ def test_windows(window, sizes):
             c.vs[c.table[s, blk], :, 0] = np.nan
     c.upload()
     q, q64 = c.rows(4, torch.float16)
-    out, lse = run(c, q, window=window)
+    out, lse = run(c, q, kernel, window=window)
     c.check_attention(q, q64, out, lse, window=window)
 
 
+@both
 @pytest.mark.parametrize("dtype", list(DTYPES))
 @pytest.mark.parametrize("spread", [0.5, 20.0, 300.0])
-def test_sinks(dtype, spread):
+def test_sinks(dtype, spread, kernel):
     """Sinks far below, among and far above the scores; rows without keys have only the sink."""
     c = Case(SIZES["drafts"] + [(40, 80)], 2, 64, seed=9).upload()
     q, q64 = c.rows(6, DTYPES[dtype])
     sinks = (torch.randn(6, generator=torch.Generator().manual_seed(1)) * spread).cuda()
-    out, lse = run(c, q, sinks=sinks)
+    out, lse = run(c, q, kernel, sinks=sinks)
     c.check_attention(q, q64, out, lse, sinks=sinks)
 
 
+@both
 @pytest.mark.parametrize("q_type", list(DTYPES))
 @pytest.mark.parametrize("out_type", list(DTYPES))
-def test_output_types(q_type, out_type):
+def test_output_types(q_type, out_type, kernel):
     c = Case([(1, 100), (50, 60)], 1, 128, seed=2).upload()
     q, q64 = c.rows(4, DTYPES[q_type])
-    out, lse = run(c, q, out_dtype=DTYPES[out_type])
+    out, lse = run(c, q, kernel, out_dtype=DTYPES[out_type])
     assert out.dtype == DTYPES[out_type]
     c.check_attention(q, q64, out, lse)
 
@@ -104,16 +120,56 @@ def test_splits(n_new, splits):
     assert torch.equal(out, again)
 
 
-def test_scores_of_any_size():
+@both
+@pytest.mark.parametrize("splits", [2, 3, 11])
+@pytest.mark.parametrize("d", [64, 128, 256, 512])
+def test_forced_splits(d, splits, kernel):
+    c = Case([(40, 700), (1, 90), (0, 10), (9, 33)], 1, d, seed=splits).upload()
+    q, q64 = c.rows(3, torch.bfloat16)
+    sinks = torch.tensor([0.5, -30.0, 4.0], device="cuda")
+    out, lse = run(c, q, kernel, splits=splits, sinks=sinks)
+    c.check_attention(q, q64, out, lse, sinks=sinks)
+    assert torch.equal(out, run(c, q, kernel, splits=splits, sinks=sinks)[0])
+
+
+@both
+def test_long_prompts(kernel):
+    """Many tiles, the workgroups' last ones partly filled, sequences that end inside a tile of rows."""
+    c = Case([(300, 300), (517, 900), (65, 1000), (1, 3)], 1, 128, seed=21, stale=np.nan).upload()
+    q, q64 = c.rows(3, torch.bfloat16)
+    out, lse = run(c, q, kernel)
+    c.check_attention(q, q64, out, lse)
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "fp32"])
+@pytest.mark.parametrize("sizes", [((1024, 1024), (700, 1500)), ((2500, 2500), (2500, 2500))])
+def test_kernels_agree(sizes, dtype):
+    """The library's choice is one of the two kernels, the tiled one for the longer prompts, and both give
+    the same within their bounds."""
+    c = Case(list(sizes), 8, 64, seed=22).upload()
+    q, _ = c.rows(32, DTYPES[dtype])
+    auto, lse = run(c, q)
+    tiled, lse1 = run(c, q, 2)
+    stream, lse2 = run(c, q, 1)
+    assert not torch.equal(tiled, stream)
+    assert torch.equal(auto, tiled) or (torch.equal(auto, stream) and sizes[0][0] < 2000)
+    vmax = 127 / 60
+    assert (tiled.float() - stream.float()).abs().max() <= 2 * vmax * (2.0 ** -11 + torch.finfo(DTYPES[dtype]).eps)
+    assert (lse1 - lse2).abs().max() <= 2.0 ** -12
+
+
+@both
+def test_scores_of_any_size(kernel):
     """Scores in the thousands (one key takes all), equal scores, and a scale of zero."""
     c = Case([(1, 300), (20, 90)], 2, 64, seed=4).upload()
     q, q64 = c.rows(2, torch.float32, spread=300.0)
     for scale in (4.0, -4.0, 0.0, 1e-30):
-        out, lse = run(c, q, scale=scale)
+        out, lse = run(c, q, kernel, scale=scale)
         c.check_attention(q, q64, out, lse, scale=scale)
 
 
-def test_scales_of_any_size():
+@both
+def test_scales_of_any_size(kernel):
     """Blocks whose scales lie far apart, zero and subnormal ones among them."""
     for lo, hi in ((-30, 30), (-140, -100), (-60, 0)):
         c = Case([(1, 400), (33, 70)], 2, 64, 16, seed=5)
@@ -122,11 +178,12 @@ def test_scales_of_any_size():
         c.ks[::4] = 0.0
         c.upload()
         q, q64 = c.rows(2, torch.float32)
-        out, lse = run(c, q)
+        out, lse = run(c, q, kernel)
         c.check_attention(q, q64, out, lse)
 
 
-def test_growing_scores():
+@both
+def test_growing_scores(kernel):
     """Each key scores above all before it by more than the slack of the running bound."""
     c = Case([(1, 200), (60, 200)], 1, 64, 16, seed=6)
     c.k[:] = 0
@@ -138,11 +195,12 @@ def test_growing_scores():
     for spread in (3.0, 100.0):
         q, _ = c.rows(1, torch.float32)
         q = q.abs() * spread
-        out, lse = run(c, q, scale=1.0)
+        out, lse = run(c, q, kernel, scale=1.0)
         c.check_attention(q, q.double().cpu().numpy(), out, lse, scale=1.0)
 
 
-def test_queries_of_any_size():
+@both
+def test_queries_of_any_size(kernel):
     """Rows of very large and small queries, of zeros, and with a NaN or an infinity: that row alone is NaN."""
     c = Case([(1, 90), (40, 64)], 1, 64, seed=7).upload()
     q, _ = c.rows(2, torch.float32)
@@ -152,37 +210,39 @@ def test_queries_of_any_size():
     q[6, 0] *= 1e-38
     q[8, 1, 4] = float("nan")
     q[9, 0, 63] = float("inf")
-    out, lse = run(c, q, scale=1.0)
+    out, lse = run(c, q, kernel, scale=1.0)
     got = out.cpu()
     bad = torch.zeros(c.n_tok, 2, dtype=torch.bool)
     bad[8, 1] = bad[9, 0] = True
     assert torch.equal(got.isnan().all(-1), bad) and torch.equal(got.isnan().any(-1), bad)
     clean = torch.where(bad[..., None].cuda(), torch.zeros_like(q), q)
-    clean_out, clean_lse = run(c, clean, scale=1.0)
+    clean_out, clean_lse = run(c, clean, kernel, scale=1.0)
     assert torch.equal(torch.where(bad[..., None], 0, clean_out.cpu()), torch.where(bad[..., None], 0, got))
     clean[3] = 0  # scores of 1e30 times the others': the one-key limit, where the plain form's bound says nothing
-    clean_out, clean_lse = run(c, clean, scale=1.0)
+    clean_out, clean_lse = run(c, clean, kernel, scale=1.0)
     c.check_attention(clean, clean.double().cpu().numpy(), clean_out, clean_lse, scale=1.0)
 
 
-def test_nan_blocks_reach_their_readers_only():
+@both
+def test_nan_blocks_reach_their_readers_only(kernel):
     c = Case([(1, 100), (90, 100), (3, 50)], 1, 64, 16, seed=8)
     c.ks[c.table[1, 3]] = np.nan   # tokens 48 .. 63
     c.vs[c.table[2, 2]] = np.nan   # tokens 32 .. 47
     c.upload()
     q, q64 = c.rows(3, torch.bfloat16)
-    out, lse = run(c, q)
+    out, lse = run(c, q, kernel)
     c.check_attention(q, q64, out, lse if False else None)
     assert out[1:39].isfinite().all() and out[39:91].isnan().all() and out[0].isfinite().all()
 
 
-def test_bad_pages_give_nan():
+@both
+def test_bad_pages_give_nan(kernel):
     c = Case([(1, 300), (1, 300), (100, 300), (1, 40)], 1, 64, 64, seed=10)
     c.table[0, 2] = -1
     c.table[2, 3] = c.k.shape[0]  # tokens 192 .. 255: the rows behind see them
     c.upload()
     q, q64 = c.rows(2, torch.float32)
-    out, lse = run(c, q)
+    out, lse = run(c, q, kernel)
     c.check_attention(q, q64, out)
     assert out[0].isnan().all() and out[1].isfinite().all() and out[2:102].isnan().all() and out[102].isfinite().all()
 
@@ -199,20 +259,21 @@ def test_rows_behind_the_last_sequence():
         assert (out[31:] == 7).all() and (lse[31:] == 7).all() and not (out[:31] == 7).any()
 
 
+@both
 @pytest.mark.parametrize("offset", [0, 1, 8])
 @pytest.mark.parametrize("dtype", list(DTYPES))
-def test_strided_queries(offset, dtype):
+def test_strided_queries(offset, dtype, kernel):
     c = Case([(20, 77), (1, 4)], 2, 64).upload()
     x, x64 = c.rows(7, DTYPES[dtype])
     flat = torch.zeros(c.n_tok, 7 * 64 + 24, dtype=DTYPES[dtype], device="cuda")
     flat[:, offset:offset + 7 * 64] = x.view(c.n_tok, -1)
     q = flat[:, offset:offset + 7 * 64].unflatten(1, (7, 64))[:, 1:5]
-    out, lse = run(c, q)
+    out, lse = run(c, q, kernel)
     c.check_attention(q, x64[:, 1:5], out, lse)
     by_head = x[:, 1:5].transpose(0, 1).contiguous().transpose(0, 1)
-    assert torch.equal(out, run(c, by_head)[0])
+    assert torch.equal(out, run(c, by_head, kernel)[0])
     same = x[:, :1].expand(-1, 4, -1)  # one query for all heads
-    out, lse = run(c, same)
+    out, lse = run(c, same, kernel)
     c.check_attention(same, np.repeat(x64[:, :1], 4, 1), out, lse)
 
 

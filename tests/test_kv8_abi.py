@@ -19,7 +19,7 @@ BAD_CACHE = [dict(n_pages=0), dict(n_pages=-1), dict(n_pages=1 << 31), dict(n_kv
              dict(head_dim=0), dict(head_dim=1024), dict(page_size=8), dict(page_size=48), dict(page_size=2048),
              dict(block=8), dict(block=24), dict(block=128), dict(page_size=1024, block=256), dict(block=0)]
 BAD_BATCH = [dict(n_seq=-1), dict(n_seq=(1 << 20) + 1), dict(n_tok=-1), dict(n_tok=(1 << 24) + 1), dict(table_width=-1),
-             dict(table_width=1 << 25), dict(max_new=-1), dict(max_len=-1), dict(starts=None)]
+             dict(table_width=(1 << 24) + 1), dict(max_new=-1), dict(max_len=-1), dict(starts=None)]
 NULLS = [("cache", dict(k_codes=None)), ("cache", dict(v_codes=None)), ("cache", dict(k_scales=None)),
          ("cache", dict(v_scales=None)), ("batch", dict(lens=None)), ("batch", dict(page_table=None))]
 MISALIGNED = [("cache", dict(k_codes=FAKE + 8)), ("cache", dict(v_codes=FAKE + 4)), ("cache", dict(k_scales=FAKE + 2)),
@@ -56,10 +56,16 @@ def calls(q8):
                                          n_q=8, window=0, scale=0.1, sinks=None, lse=None), **args})
         return lib.kv8_attention(c, b, ctypes.byref(a), ws, ws_bytes, None)
 
+    def debug(cache=None, batch=None, ws=None, ws_bytes=0, kernel=1, splits=0, **args):
+        c, b, keep = structs(cache, batch)
+        a = kv8._AttentionArgs(**{**dict(out=FAKE, q=FAKE, q_token_stride=1024, q_head_stride=128, out_type=1, q_type=1,
+                                         n_q=8, window=0, scale=0.1, sinks=None, lse=None), **args})
+        return lib.kv8_attention_debug(c, b, ctypes.byref(a), ws, ws_bytes, kernel, splits, None)
+
     def workspace(cache=None, batch=None, n_q=8):
         c, b, keep = structs(cache, batch)
         return lib.kv8_attention_workspace_bytes(c, b, n_q)
-    return dict(write=write, read=read, attention=attention, workspace=workspace)
+    return dict(write=write, read=read, attention=attention, debug=debug, workspace=workspace)
 
 
 def test_exports_every_declared_symbol(q8):
@@ -112,6 +118,15 @@ def test_attention_refusals(q8, calls):
     for bad in (dict(out=FAKE + 8), dict(q=FAKE + 1), dict(sinks=FAKE + 2), dict(lse=FAKE + 2), dict(ws=FAKE + 8, ws_bytes=64),
                 dict(q=FAKE + 2, q_type=0)):
         assert f(**bad) == q8.Q8_0_EALIGN, bad
+
+
+def test_debug_refusals(q8, calls):
+    f = calls["debug"]
+    for bad in (dict(kernel=3), dict(kernel=-1), dict(splits=-1), dict(splits=257), dict(kernel=0, splits=2), dict(n_q=7),
+                dict(kernel=2, cache=dict(head_dim=512), q_type=0), dict(splits=2, batch=dict(n_tok=1 << 18), n_q=8)):
+        assert f(**bad) == q8.Q8_0_EINVAL, bad
+    assert f(splits=2, ws=FAKE, ws_bytes=2 * 5 * 8 * 129 * 4 - 1) == q8.Q8_0_EWORKSPACE
+    assert f(splits=2) == q8.Q8_0_EWORKSPACE
 
 
 def test_null_structs(q8):
