@@ -92,10 +92,12 @@ size_t partial_bytes(const Cache &c, const Batch &b, int n_q, int splits) {
 //   tiled: a unit takes `tile` for `keys` keys of all its rows, `at_once` workgroups beside each other.
 // Both take some us before the first key and behind the last, the join of splits some more, and its traffic.
 // What the estimates decide, measured (us, stream / tiled): heads of 128, 8 of them, groups of 4: 256 tokens
-// 9 / 18; 2 x 1000 tokens 90 / 41; 40 sequences of 32 tokens over 2000 keys 117 / 195; 8192 tokens
-// 1368 / 610.  Heads of 512, 64 on one, 2 x 300 tokens over 1000 keys 322 / 240; 12 single tokens over up
-// to 6000 keys 56 / 80.  Splits of one sequence of 2000 keys, 1 / 4 / 16: 20 / 12 / 10; of 131072 keys, 16 / 64:
-// 82 / 48; of 64 sequences of up to 8192, 1 / 4: 133 / 137.
+// 9 / 19; 2 x 1000 tokens 69 / 58; 40 sequences of 32 tokens over 2000 keys 123 / 178; 8192 tokens
+// 1368 / 610.  Heads of 512, 64 on one, 2 x 300 tokens over 4000 keys 946 / 808; 12 single tokens over up
+// to 6000 keys 57 / 78.  Splits of the stream kernel, one sequence of 2000 keys, 1 / 4 / 16: 20 / 12 / 10; of
+// 131072 keys, 16 / 64: 82 / 48; of 64 sequences of up to 8192, 1 / 4: 133 / 137.  Splits of the tiled kernel,
+// 512 tokens over 32768 keys, 1 / 2 / 4 / 8: 883 / 457 / 285 / 303 (stream, at its best, 668); 2048 over
+// 16384, 1 / 2: 526 / 538.
 struct Cost {
   float alone, shared, tile;
   int keys, at_once;
@@ -107,7 +109,7 @@ Cost cost_of(int d, bool halves) {
     case 128: return {1.2f * more, 0.75f * more, 2.4f * more, 64, 1};
     case 192: return {1.6f * more, 1.1f * more, 2.2f * more, 32, 1};
     case 256: return {2.0f * more, 1.55f * more, 2.6f * more, 32, 1};
-    default: return {3.0f * more, 3.0f * more, 2.7f * more, 32, 1};
+    default: return {3.0f * more, 3.0f * more, 2.2f * more, 32, 1};
   }
 }
 
@@ -116,8 +118,15 @@ Plan attention_plan(const Cache &c, const Batch &b, int n_q, int window, bool ha
   const Cost cost = cost_of(c.d, halves);
   const int group = n_q / c.n_kv;
   const int64_t most_rows = (int64_t)b.max_new * group;
-  auto workgroups = [&](int rows) {
-    return (float)((most_rows > rows ? (int64_t)b.n_tok * group / rows + b.n_seq : b.n_seq) * c.n_kv);
+  // Workgroups launched for tiles of `rows` rows: each sequence's last ones share none, so some find no rows.
+  // The tiled kernel starts those first and they are gone when the others need their units; the stream
+  // kernel's lie between the others (12 tokens of 64 heads on one: 60 launched, 48 with rows; 4 splits 52 us, 5 62).
+  auto launched = [&](int rows) {
+    return most_rows > rows ? (int64_t)b.n_tok * group / rows + b.n_seq : b.n_seq;
+  };
+  auto with_rows = [&](int rows) {
+    const int64_t all = (most_rows / rows + (most_rows % rows != 0)) * b.n_seq;
+    return all < launched(rows) ? all : launched(rows);
   };
   // keys of the longest row tile, and of a mean one: rows of a prompt see half of it
   float longest = (float)b.max_len;
@@ -127,7 +136,7 @@ Plan attention_plan(const Cache &c, const Batch &b, int n_q, int window, bool ha
 
   Plan best{false, 1};
   float least = INFINITY;
-  const float streams = workgroups(16);
+  const float streams = (float)(launched(16) * c.n_kv);
   const bool many = (int64_t)b.n_tok * n_q > kMaxJoinRows;
   const int units = (b.max_len + 127) / 128;  // of 128 keys, a step of a workgroup's four waves
   for (int each = units; each >= 1; each -= each > 8 ? (each + 7) / 8 : 1) {
@@ -144,10 +153,20 @@ Plan attention_plan(const Cache &c, const Batch &b, int n_q, int window, bool ha
     }
   }
   if (!(halves && c.d > 256)) {  // its operands do not fit the registers
-    const float each = workgroups(tile_rows(c.d, halves)) / (kUnits * cost.at_once);
-    const float rounds = prompt ? fmaxf(1.f, each) : ceilf(each);
-    const float t = fmaxf(longest / cost.keys * cost.tile + kTileEnds, rounds * (mean / cost.keys * cost.tile + kTileEnds));
-    if (t < least) best = {true, 1};
+    const float tiles = (float)(with_rows(tile_rows(c.d, halves)) * c.n_kv);
+    for (int splits = 1; splits <= 64 && (splits == 1 || (!many && splits <= units)); ++splits) {
+      const float bytes = (float)partial_bytes(c, b, n_q, splits);
+      if (bytes > (float)ws_bytes) break;
+      const float each = tiles * splits / (kUnits * cost.at_once);
+      const float rounds = prompt ? fmaxf(1.f, each) : ceilf(each);
+      const float one = cost.tile / (cost.keys * (float)splits);
+      const float t = fmaxf(longest * one + kTileEnds, rounds * (mean * one + kTileEnds)) +
+                      (splits > 1 ? kJoin + 2.f * bytes / kJoinBytes : 0.f);
+      if (t < least) {
+        least = t;
+        best = {true, splits};
+      }
+    }
   }
   return best;
 }

@@ -144,15 +144,16 @@ def test_long_prompts(kernel):
 @pytest.mark.parametrize("dtype", ["bf16", "fp32"])
 @pytest.mark.parametrize("sizes", [((1024, 1024), (700, 1500)), ((2500, 2500), (2500, 2500))])
 def test_kernels_agree(sizes, dtype):
-    """The library's choice is one of the two kernels, the tiled one for the longer prompts, and both give
-    the same within their bounds."""
+    """The library's choice is one of the two kernels, the tiled one (with some splits or none) for the longer
+    prompts, and both give the same within their bounds."""
     c = Case(list(sizes), 8, 64, seed=22).upload()
     q, _ = c.rows(32, DTYPES[dtype])
     auto, lse = run(c, q)
     tiled, lse1 = run(c, q, 2)
     stream, lse2 = run(c, q, 1)
     assert not torch.equal(tiled, stream)
-    assert torch.equal(auto, tiled) or (torch.equal(auto, stream) and sizes[0][0] < 2000)
+    assert (any(torch.equal(auto, run(c, q, 2, splits=n)[0]) for n in (1, 2, 3, 4))
+            or (torch.equal(auto, stream) and sizes[0][0] < 2000))
     vmax = 127 / 60
     assert (tiled.float() - stream.float()).abs().max() <= 2 * vmax * (2.0 ** -11 + torch.finfo(DTYPES[dtype]).eps)
     assert (lse1 - lse2).abs().max() <= 2.0 ** -12
@@ -378,6 +379,56 @@ def test_side_stream():
         got = c.q8.kv8_attention(c.cache, c.batch, q)
     side.synchronize()
     assert torch.equal(got, want)
+
+
+@pytest.mark.parametrize("splits", [1, 3])
+def test_tiled_prompts_in_a_graph(splits):
+    """The tiled kernel captured on a side stream and replayed while lengths and starts move, two graphs on
+    one workspace, eager work in between; rows behind the last sequence stay."""
+    c = Case([(70, 300), (40, 500)], 1, 128, seed=23)
+    c.n_tok = 130
+    c.upload()
+    lens, starts = (torch.from_numpy(a.copy()).cuda() for a in (c.lens, c.starts))
+    batch = c.q8.Kv8Batch(c.batch.page_table, lens, starts, n_tok=130, max_new=130)
+    q, q64 = c.rows(4, torch.bfloat16)
+    ws = torch.empty(splits * 130 * 4 * 129 * 4, dtype=torch.uint8, device="cuda")
+    outs, graphs = [torch.empty_like(q) for _ in range(2)], []
+    for out, window in zip(outs, (0, 100)):
+        g = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(g, stream=torch.cuda.Stream()):
+            c.q8.kv8_attention_debug(c.cache, batch, q, 2, splits=splits, window=window, out=out, workspace=ws)
+        graphs.append(g)
+    for news, lengths in (((70, 40), (300, 500)), ((1, 129), (64, 448)), ((0, 3), (0, 3)), ((128, 1), (290, 1))):
+        c.lens, c.starts = np.array(lengths, np.int32), np.array([0, news[0], sum(news)], np.int32)
+        lens.copy_(torch.from_numpy(c.lens)), starts.copy_(torch.from_numpy(c.starts))
+        n = sum(news)
+        for out in outs:
+            out.fill_(7)
+        for g in graphs:
+            g.replay()
+        eager = c.q8.kv8_attention_debug(c.cache, batch, q, 2, splits=splits, workspace=ws)
+        torch.cuda.synchronize()
+        for out, window in zip(outs, (0, 100)):
+            assert (out[n:] == 7).all()
+            c.check_attention(q[:n], q64[:n], out[:n], window=window)
+        assert torch.equal(eager[:n], outs[0][:n])
+
+
+def test_long_cache_chunk_takes_splits():
+    """Few rows over many keys: the tiled kernel with splits, the workspace's size deciding how many."""
+    c = Case([(256, 6000)], 4, 64, seed=24).upload()
+    q, _ = c.rows(16, torch.bfloat16)
+    ws = c.q8.kv8_attention_workspace(c.cache, c.batch, 16)
+    one = 256 * 16 * 65 * 4
+    assert ws.numel() >= 2 * one and ws.numel() % one == 0
+    auto, lse = run(c, q, workspace=ws)
+    tiled, lse1 = run(c, q, 2, splits=ws.numel() // one, workspace=ws)
+    assert torch.equal(auto, tiled) and torch.equal(lse, lse1)
+    vmax = 127 / 60
+    for less in (2 * one, 0):
+        out, lse1 = run(c, q, workspace=ws[:less])
+        assert (out.float() - auto.float()).abs().max() <= 2 * vmax * (2.0 ** -11 + torch.finfo(q.dtype).eps)
+        assert (lse1 - lse).abs().max() <= 2.0 ** -12
 
 
 def test_lse_joins_two_caches():
