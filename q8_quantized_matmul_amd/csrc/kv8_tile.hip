@@ -16,9 +16,9 @@
 // t while it scales the scores of t + 1 and puts the tiles that come next into LDS.  K is therefore staged
 // a tile ahead of V; each has two buffers, and there is one barrier a step.
 //
-// Measured, causal, 32 heads of 128 on 8, bf16: 8192 tokens 561 us (980 TFLOP/s of the live half), 32768
+// Measured, causal, 32 heads of 128 on 8, bf16: 8192 tokens 560 to 610 us (900 to 980 TFLOP/s of the live half), 32768
 // tokens 8.4 to 8.7 ms (1.0 PFLOP/s); torch's product of two fp16 matrices of 8192 reaches 1.17 on the same card.
-// Both run at about 2.0 GHz.  On the way there (8192 tokens): weights, then products, tile by tile 806 us; page ids
+// Both run at about 2.0 GHz.  512 tokens over 32768 keys, split in four, 288 us (957 TFLOP/s).  On the way there (8192 tokens): weights, then products, tile by tile 806 us; page ids
 // looked up a tile ahead of the codes, which nothing then waits for, 647; both at once 617.  Not taken, all within 5 %
 // of it or slower: deeper operand reads, a fixed order of products and vector work with scores of two tiles in
 // registers (their spills wait for the loads in flight), sums by dot products (they run on the matrix core), four
