@@ -41,7 +41,7 @@ __global__ __launch_bounds__(256) void stream_kernel(Cache c, Batch b, Attention
   }
   const Span q = span_of(b, c, s);
   const int rows = q.n * a.group, r0 = tile * kRows;
-  if (r0 >= rows) return;
+  if (r0 < 0 || r0 >= rows) return;  // below 0: starts that do not ascend from 0
   const int tok_hi = (min(r0 + kRows, rows) - 1) / a.group;
   const int row = r0 + col, tok = min(row / a.group, tok_hi);
   const bool row_ok = row < rows;

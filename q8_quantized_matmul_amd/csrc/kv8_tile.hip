@@ -85,7 +85,7 @@ __global__ __launch_bounds__((Shape<D, HALVES>::kThreads), (Shape<D, HALVES>::kW
   const int s = find_sequence(b, slots, w);
   const Span q = span_of(b, c, s);
   const int rows = q.n * a.group, r0 = (int)(w - slots.first(b, s)) * S::kRows;
-  if (r0 >= rows) return;
+  if (r0 < 0 || r0 >= rows) return;  // below 0: starts that do not ascend from 0
   const int wg_hi = q.first + (min(r0 + S::kRows, rows) - 1) / a.group, wg_lo = q.first + r0 / a.group;
   const int wr0 = r0 + 32 * (wave / kParts);
   const bool wave_ok = wr0 < rows;

@@ -431,6 +431,37 @@ def test_long_cache_chunk_takes_splits():
         assert (lse1 - lse).abs().max() <= 2.0 ** -12
 
 
+@both
+def test_rows_before_the_first_sequence(kernel):
+    """starts[0] above 0 (which the contract excludes): no row outside the sequences is touched, query heads far
+    apart, and the sequences' rows come out as ever."""
+    c = Case([(40, 200), (9, 90)], 1, 64, seed=25).upload()
+    q, q64 = c.rows(3, torch.bfloat16)
+    apart = torch.randn(3, 49 + 50, 64, device="cuda").bfloat16()  # [head][token]
+    apart[:, 50:] = q.transpose(0, 1)
+    qs = apart.transpose(0, 1)
+    starts = torch.from_numpy(c.starts + 50).int().cuda()
+    b = c.q8.Kv8Batch(c.batch.page_table, c.batch.lens, starts, n_tok=99, max_new=40)
+    out, lse = torch.full((99, 3, 64), 7.0, device="cuda", dtype=torch.bfloat16), torch.full((99, 3), 7.0, device="cuda")
+    c.q8.kv8_attention_debug(c.cache, b, qs, kernel, out=out, lse=lse)
+    torch.cuda.synchronize()
+    assert (out[:50] == 7).all() and (lse[:50] == 7).all()
+    c.check_attention(q, q64, out[50:], lse[50:])
+
+
+@both
+def test_starts_in_no_order(kernel):
+    """Rows of every sequence are read and written within the arrays, whatever starts holds."""
+    c = Case([(30, 100), (30, 100), (30, 100)], 1, 64, seed=26).upload()
+    q, _ = c.rows(3, torch.bfloat16)
+    for starts in ((0, 80, 20, 90), (70, 3, 90, 1), (-5, 500, 60, 30)):
+        b = c.q8.Kv8Batch(c.batch.page_table, c.batch.lens, torch.tensor(starts, dtype=torch.int32, device="cuda"), n_tok=90)
+        out = torch.empty(92, 3, 64, device="cuda", dtype=torch.bfloat16).fill_(7)
+        c.q8.kv8_attention_debug(c.cache, b, q, kernel, out=out[1:91])
+        torch.cuda.synchronize()
+        assert (out[0] == 7).all() and (out[91] == 7).all()
+
+
 def test_lse_joins_two_caches():
     """What lse is for: attention over two halves of the keys joined by their sums."""
     c = Case([(1, 256)], 1, 64, 64, seed=15).upload()
