@@ -142,11 +142,11 @@ Plan attention_plan(const Cache &c, const Batch &b, int n_q, int window, bool ha
   for (int each = units; each >= 1; each -= each > 8 ? (each + 7) / 8 : 1) {
     const int splits = (units + each - 1) / each;
     if (splits > 256 || (many && splits > 1)) break;
-    const float bytes = (float)partial_bytes(c, b, n_q, splits);
-    if (bytes > (float)ws_bytes) continue;
+    const size_t bytes = partial_bytes(c, b, n_q, splits);
+    if (bytes > ws_bytes) continue;  // (fp32 does not hold every size: the kernels would write past the workspace)
     const float rounds = prompt ? fmaxf(1.f, streams * splits / kUnits) : ceilf(streams * splits / kUnits);
     const float t = fminf((float)each, ceilf(mean / 128.f)) * fmaxf(cost.alone, cost.shared * rounds) + kEnds * fmaxf(1.f, rounds / 4.f) +
-                    (splits > 1 ? kJoin + 2.f * bytes / kJoinBytes : 0.f);
+                    (splits > 1 ? kJoin + 2.f * (float)bytes / kJoinBytes : 0.f);
     if (t < least) {
       least = t;
       best.splits = splits;
@@ -155,13 +155,13 @@ Plan attention_plan(const Cache &c, const Batch &b, int n_q, int window, bool ha
   if (!(halves && c.d > 256)) {  // its operands do not fit the registers
     const float tiles = (float)(with_rows(tile_rows(c.d, halves)) * c.n_kv);
     for (int splits = 1; splits <= 64 && (splits == 1 || (!many && splits <= units)); ++splits) {
-      const float bytes = (float)partial_bytes(c, b, n_q, splits);
-      if (bytes > (float)ws_bytes) break;
+      const size_t bytes = partial_bytes(c, b, n_q, splits);
+      if (bytes > ws_bytes) break;
       const float each = tiles * splits / (kUnits * cost.at_once);
       const float rounds = prompt ? fmaxf(1.f, each) : ceilf(each);
       const float one = cost.tile / (cost.keys * (float)splits);
       const float t = fmaxf(longest * one + kTileEnds, rounds * (mean * one + kTileEnds)) +
-                      (splits > 1 ? kJoin + 2.f * bytes / kJoinBytes : 0.f);
+                      (splits > 1 ? kJoin + 2.f * (float)bytes / kJoinBytes : 0.f);
       if (t < least) {
         least = t;
         best = {true, splits};
