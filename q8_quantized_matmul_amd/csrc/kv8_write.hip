@@ -127,6 +127,7 @@ __global__ __launch_bounds__(kWriteThreads(BLOCK_WAVES)) void write_kernel(Cache
     const Slots slots{kBlock, 1, 2};
     s = find_sequence(b, slots, blockIdx.x);
     nth = (int)(blockIdx.x - slots.first(b, s));
+    if (nth < 0) return;  // starts that do not ascend from 0: a block before the table's first
   }
   const Span q = span_of(b, c, s);
   const int base = (max(q.first, 0) >> c.block_log << c.block_log) + nth * kBlock;
@@ -246,7 +247,8 @@ __global__ __launch_bounds__(256) void read_kernel(Cache c, Batch b, void *k, vo
     nth = (int)(blockIdx.x - slots.first(b, s));
   }
   const Span q = span_of(b, c, s);
-  // positions below 0 (a sequence with more rows than tokens) make blocks of their own
+  // positions below 0 (a sequence with more rows than tokens) make blocks of their own; where nth is below 0, t0 is
+  // 16 at least
   const int base = (q.first >> 4 << 4) + nth * 16;
   const int t0 = max(q.first - base, 0), t1 = min(q.len - base, 16);
   if (t0 >= t1) return;
