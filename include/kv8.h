@@ -129,8 +129,11 @@ size_t kv8_attention_workspace_bytes(const kv8_cache *cache, const kv8_batch *ba
  * Numbers: codes enter the matrix core exactly as fp16, queries as fp16 under a
  * power of two per row (16-bit queries exactly, but for values below 2^-28 of the
  * row's largest), fp32 queries as two such halves; exp, sums and outputs are fp32.
- * Weights are rounded to fp16 (11 bits) for 16-bit outputs and queries, and kept in
- * two halves (22 bits) where out_type or q_type is KV8_F32.
+ * A key's weight and V scale become one factor under the largest V scale that the row
+ * sees.  It is rounded to fp16 (11 bits) for 16-bit outputs and queries, and kept in
+ * two halves (22 bits) where out_type or q_type is KV8_F32, either way no finer than
+ * 2^-31 of the largest weight under that scale (so values of V lose some of the 11 bits from
+ * 2^21 below others that the row sees on, some of the 22 from 2^10 below).
  *   workspace / workspace_bytes : optional scratch, 16-byte aligned device memory, its
  *     contents on entry do not matter.  With less than
  *     kv8_attention_workspace_bytes() a plan with fewer splits that fits is taken;

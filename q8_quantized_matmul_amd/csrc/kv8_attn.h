@@ -6,7 +6,8 @@
 // all but the smallest keep its 11 bits.  The bound moves only when a score passes it by kSlack,
 // which is rare, so most steps neither reduce a maximum over lanes nor rescale their sums.
 // V's scales enter the weights as vs * 2^-E, at most 1, E being the exponent of the largest
-// scale seen so far (the same for all rows); a growth of E rescales the sums exactly.
+// scale that the row has seen so far; a growth of E rescales the sums exactly.  E belongs to the row:
+// blocks that only later rows of a tile see, or that lie before a row's window, may have any scale.
 #pragma once
 
 #include "kv8_device.h"
@@ -75,7 +76,7 @@ struct RowScale {
 struct Finish {
   float lse2;    // log2 of the sum of exp2(score), the sink among them
   float factor;  // output = sum * factor
-  // m: the row's bound; e: the exponent taken out of V's scales; sink2: log2 units, or -inf
+  // m: the row's bound; e: its exponent taken out of V's scales; sink2: log2 units, or -inf
   __device__ __forceinline__ Finish(float m, float total, int e, float sink2) {
     lse2 = total == 0.f ? -INFINITY : m - kBias + log2_fast(total);
     factor = total == 0.f ? 0.f : ldexp_fast(1.f / total, e);

@@ -27,7 +27,7 @@ __global__ __launch_bounds__(256) void stream_kernel(Cache c, Batch b, Attention
   constexpr int kChunks = D / 64;
   __shared__ float join_o[kWaves][64][kRows + 1];
   __shared__ float join_m[kWaves][kRows], join_l[kWaves][kRows];
-  __shared__ int join_e[kWaves];
+  __shared__ int join_e[kWaves][kRows];
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
   const int g = lane >> 4, col = lane & 15;
   const int head = blockIdx.x % c.n_kv, w = blockIdx.x / c.n_kv, split = blockIdx.y;
@@ -166,8 +166,17 @@ __global__ __launch_bounds__(256) void stream_kernel(Cache c, Batch b, Attention
 #pragma unroll
         for (int i = 0; i < 4 * kChunks; ++i) o[i] *= f;
       }
-      const int e2 = max(__builtin_amdgcn_readlane(exponent, 2 * t), __builtin_amdgcn_readlane(exponent, 2 * t + 1));
-      if (e2 > e) {
+      int e2 = max(__builtin_amdgcn_readlane(exponent, 2 * t), __builtin_amdgcn_readlane(exponent, 2 * t + 1));
+      if (ragged) {  // by row: of the 16 keys that it sees one of
+        e2 = kNoScale;
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+          const int j = key + 16 * h;
+          if (j <= pos && (!a.window || j + 15 > pos - a.window)) e2 = max(e2, __builtin_amdgcn_readlane(exponent, 2 * t + h));
+        }
+      }
+      if (__any(e2 > e)) {
+        e2 = max(e, e2);
         const float f = ldexp_fast(1.f, e - e2);
         e = e2;
 #pragma unroll
@@ -202,8 +211,8 @@ __global__ __launch_bounds__(256) void stream_kernel(Cache c, Batch b, Attention
   if (g == 0) {
     join_m[wave][col] = m;
     join_l[wave][col] = l;
+    join_e[wave][col] = e;
   }
-  if (lane == 0) join_e[wave] = e;
   __syncthreads();
   const int jr = threadIdx.x >> 4, jd = (threadIdx.x & 15) * 4;
   float jm = kLowest, jl = 0.f, jf[kWaves];
@@ -211,13 +220,13 @@ __global__ __launch_bounds__(256) void stream_kernel(Cache c, Batch b, Attention
 #pragma unroll
   for (int i = 0; i < kWaves; ++i) {
     jm = fmaxf(jm, join_m[i][jr]);
-    je = max(je, join_e[i]);
+    je = max(je, join_e[i][jr]);
   }
 #pragma unroll
   for (int i = 0; i < kWaves; ++i) {
     const float f = exp2_fast(join_m[i][jr] - jm);
     jl += join_l[i][jr] * f;
-    jf[i] = ldexp_fast(f, join_e[i] - je);
+    jf[i] = ldexp_fast(f, join_e[i][jr] - je);
   }
   const int j_row = r0 + jr, j_tok = j_row / a.group, j_head = head * a.group + j_row % a.group;
   const bool j_ok = j_row < rows;

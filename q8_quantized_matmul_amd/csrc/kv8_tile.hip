@@ -58,9 +58,9 @@ struct Shape {
   static constexpr int kTile = kKeys * D;                  // fp16 values of a K or V tile
   static constexpr int kChunks = kKeys * D / 16;           // 16-byte pieces of codes of a K or V tile
   static constexpr int kPasses = (kChunks + kThreads - 1) / kThreads;
-  static constexpr int kScaleWords = (3 * kGroups + 2 + 3) / 4 * 4;
+  static constexpr int kScaleWords = (4 * kGroups + 2 + 3) / 4 * 4;
   static constexpr int kMeet = kParts > 1 ? kWaves * 16 * 64 : 0;  // fp32 scores of the waves
-  static constexpr int kLds = 2 * (2 * kTile * 2 + kScaleWords * 4) + kMeet * 4;
+  static constexpr int kLds = 2 * (2 * kTile * 2 + kScaleWords * 4) + kMeet * 4 + kRows * 4;
 };
 
 template <int D, bool HALVES>
@@ -74,6 +74,7 @@ __global__ __launch_bounds__((Shape<D, HALVES>::kThreads), (Shape<D, HALVES>::kW
   _Float16 *const vt = kt + 2 * S::kTile;                     // [2][kTile]
   float *const scales = reinterpret_cast<float *>(vt + 2 * S::kTile);  // [2][kScaleWords], see put
   float *const meet = scales + 2 * S::kScaleWords;                     // [wave][16][64]
+  int *const positions = reinterpret_cast<int *>(meet + S::kMeet);     // [kRows]
   const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
   const int part_of = wave % kParts, dim0 = part_of * S::kDims;  // this wave's dims
   const int half = lane >> 5, col = lane & 31;
@@ -93,7 +94,10 @@ __global__ __launch_bounds__((Shape<D, HALVES>::kThreads), (Shape<D, HALVES>::kW
   const int row = wr0 + col, tok = min(row / a.group, tok_hi);
   const bool row_ok = row < rows;
   const int q_head = head * a.group + (row_ok ? row - tok * a.group : 0);
-  const int pos = row_ok ? q.first + tok : -1;
+  // The row's position is wanted where masks are and at the end: until then it lies in LDS, each wave's own (a
+  // register more, and heads of 128 spill).
+  positions[wr0 - r0 + col] = row_ok ? q.first + tok : -1;
+  auto position = [&] { return positions[wr0 - r0 + (threadIdx.x & 31)]; };
   const int pos_lo = q.first + wr0 / a.group, pos_hi = wave_ok ? q.first + tok_hi : -1;
 
   // the keys: n tiles from first_key on, counted from 0 below
@@ -213,8 +217,9 @@ __global__ __launch_bounds__((Shape<D, HALVES>::kThreads), (Shape<D, HALVES>::kW
   };
   // Of each group: K's scale; with E the largest exponent of the tile's scales of V, log2(V's / 2^E), which goes
   // into the weights' exponent, and 2^E / V's, by which a group's sum of weights is multiplied again: an
-  // addition less for each weight than a product.  Of the tile: E, and the least exponent (kNoFold where a
-  // scale is zero, no number, or under 2^-8 of another: weights vanish there that the rows' sums need).
+  // addition less for each weight than a product; V's itself, for rows that do not see every group.  Of the tile:
+  // E, and the least exponent (kNoFold where a scale is zero, no number, or under 2^-8 of another: weights vanish
+  // there that the rows' sums need).
   auto put_scales = [&](int t, const Scales &g) {
     if (wave != 0) return;
     const int i = lane % kGroups;
@@ -233,9 +238,10 @@ __global__ __launch_bounds__((Shape<D, HALVES>::kThreads), (Shape<D, HALVES>::kW
       sc[lane] = g.k;
       sc[kGroups + lane] = log2_fast(v);
       sc[2 * kGroups + lane] = absent ? 0.f : __builtin_amdgcn_rcpf(v);
+      sc[3 * kGroups + lane] = g.v;
     }
     if (lane == 0) {
-      int *const of_tile = reinterpret_cast<int *>(sc + 3 * kGroups);
+      int *const of_tile = reinterpret_cast<int *>(sc + 4 * kGroups);
       of_tile[0] = most;
       of_tile[1] = least;
     }
@@ -352,12 +358,16 @@ __global__ __launch_bounds__((Shape<D, HALVES>::kThreads), (Shape<D, HALVES>::kW
   // y of tile t from its products, before the rare cases below
   float fk[kGroups], lw[kGroups];
   int e_next, least;
+  int e_low = kNoScale, e_high = kNoScale;  // of the wave's rows
+  bool unset = true;                        // some row has no bound
+  bool odd;                                 // y is not all (rare_cases)
   auto tile_scales = [&](int t) {
     const float *const sc = scales + (t & 1) * S::kScaleWords;
-    const int *const of_tile = reinterpret_cast<const int *>(sc + 3 * kGroups);
+    const int *const of_tile = reinterpret_cast<const int *>(sc + 4 * kGroups);
     const int most = __builtin_amdgcn_readfirstlane(of_tile[0]);
     least = __builtin_amdgcn_readfirstlane(of_tile[1]);
     e_next = max(e, most);
+    odd = unset || most > e_low || least < e_high - kFoldBits;
     const float shift = (float)(most - e_next), back = ldexp_fast(1.f, e_next - most);
 #pragma unroll
     for (int i = 0; i < kGroups; ++i) {
@@ -376,41 +386,59 @@ __global__ __launch_bounds__((Shape<D, HALVES>::kThreads), (Shape<D, HALVES>::kW
 #pragma unroll
       for (int j = 0; j < 16; ++j) y[sub][j] = __builtin_fmaf(z[sub][j], fk[2 * sub + (j >> 3)], add[2 * sub + (j >> 3)]);
   };
-  // What is not in every tile: keys that some row of the wave does not see, a scale of V above all
-  // before, a row's first keys (its bound is not set), scales that do not fold.
+  // What is not in every tile: keys that some row of the wave does not see, a scale of V above all that some row
+  // has seen, a row's first keys (its bound is not set), scales that do not fold.  (One branch for all of them, on
+  // scalars: a vote over the rows' exponents and bounds in every tile took 8192 tokens from 565 to 578 us.)
   auto rare_cases = [&](int t, const f32x16 (&z)[kSubs]) {
     const int key = first_key + t * S::kKeys;
+    const float *const sc = scales + (t & 1) * S::kScaleWords;
     const bool ragged = key + S::kKeys - 1 > pos_lo || (a.window && key <= pos_hi - a.window);
-    auto unseen = [&](int sub, int j) {
+    auto unseen = [&](int pos, int sub, int j) {
       const int at = key + 32 * sub + 8 * (j >> 2) + 4 * half + (j & 3);
       return at > pos || (a.window && at <= pos - a.window);
     };
+    if (!ragged && !odd) return;
+    rare();
+    const int pos = position();
+    int low = least;
     if (ragged) {
-      rare();
+      // a row's exponents are those of the groups that it sees; the others may have any scale
+      auto sees = [&](int i) { return key + 16 * i <= pos && !(a.window && key + 16 * i + 15 <= pos - a.window); };
+      auto exponent = [&](float v) { return v > 0.f && v < INFINITY ? exponent_of(v) : kNoScale; };
+      e_next = e;
+      low = -kNoFold;
 #pragma unroll
-      for (int sub = 0; sub < kSubs; ++sub)
+      for (int i = 0; i < kGroups; ++i) {
+        const int at = exponent(sc[3 * kGroups + i]);
+        e_next = sees(i) ? max(e_next, at) : e_next;
+        low = sees(i) ? min(low, at == kNoScale ? kNoFold : at) : low;
+      }
+      asm volatile("" ::: "memory");  // (read again below: four registers less)
+      const float mb = m - kBias;
 #pragma unroll
-        for (int j = 0; j < 16; ++j) y[sub][j] = unseen(sub, j) ? -INFINITY : y[sub][j];
-      // groups that no row sees may have any scale
+      for (int i = 0; i < kGroups; ++i) {
+        const int at = exponent(sc[3 * kGroups + i]);
+        const float v = ldexp_fast(sc[3 * kGroups + i], -at);
+        lw[i] = log2_fast(v) + (float)(at - e_next);
+        share[i] = sees(i) ? ldexp_fast(__builtin_amdgcn_rcpf(v), e_next - at) : 0.f;
 #pragma unroll
-      for (int i = 0; i < kGroups; ++i)
-        if (key + 16 * i > pos_hi || (a.window && key + 16 * i + 15 <= pos_lo - a.window)) share[i] = 0.f;
+        for (int j = 8 * (i & 1); j < 8 * (i & 1) + 8; ++j)
+          y[i >> 1][j] = unseen(pos, i >> 1, j) ? -INFINITY : __builtin_fmaf(z[i >> 1][j], fk[i], lw[i] - mb);
+      }
     }
-    if (e_next > e) {
-      rare();
+    if (__any(e_next > e)) {
       scale_sums(ldexp_fast(1.f, e - e_next));
       e = e_next;
     }
-    const bool unfolded = least < e - kFoldBits;
+    const bool unfolded = __any(low < e - kFoldBits);
     if (unfolded || __any(m == kLowest)) {
-      rare();
       float top = kLowest;
 #pragma unroll
       for (int sub = 0; sub < kSubs; ++sub)
 #pragma unroll
         for (int j = 0; j < 16; ++j) {
           const float x = __builtin_fmaf(z[sub][j], fk[2 * sub + (j >> 3)], 0.f);
-          y[sub][j] = unseen(sub, j) ? -INFINITY : x;
+          y[sub][j] = unseen(pos, sub, j) ? -INFINITY : x;
           top = fmaxf(top, y[sub][j]);
         }
       top = fmaxf(top, __shfl_xor(top, 32));
@@ -433,6 +461,10 @@ __global__ __launch_bounds__((Shape<D, HALVES>::kThreads), (Shape<D, HALVES>::kW
         for (int i = 0; i < kGroups; ++i) share[i] = 0.f;
       }
     }
+    unset = __any(m == kLowest);
+    e_low = e_high = __builtin_amdgcn_readfirstlane(e);
+    while (const uint64_t below = __ballot(e < e_low)) e_low = __builtin_amdgcn_readlane(e, __builtin_ctzll(below));
+    while (const uint64_t above = __ballot(e > e_high)) e_high = __builtin_amdgcn_readlane(e, __builtin_ctzll(above));
   };
 
   if (n > 0) {
@@ -492,9 +524,12 @@ __global__ __launch_bounds__((Shape<D, HALVES>::kThreads), (Shape<D, HALVES>::kW
   }
 
   l += __shfl_xor(l, 32);
-  if (!row_ok) return;
-  const int64_t at = (int64_t)(q.row0 + tok) * a.n_q + q_head;
-  const Finish fin(m, l, e, splits == 1 && a.sinks ? a.sinks[q_head] * kLog2e : -INFINITY);
+  // the row again: nothing of it but its position was kept
+  const int out_row = wr0 + (threadIdx.x & 31), out_tok = position() - q.first;
+  if (out_row >= rows) return;
+  const int out_head = head * a.group + out_row - out_tok * a.group;
+  const int64_t at = (int64_t)(q.row0 + out_tok) * a.n_q + out_head;
+  const Finish fin(m, l, e, splits == 1 && a.sinks ? a.sinks[out_head] * kLog2e : -INFINITY);
   const Partials part(ws, b, c, a.n_q, splits);
   if (half == 0 && part_of == 0) {
     if (splits > 1)

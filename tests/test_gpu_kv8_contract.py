@@ -6,7 +6,7 @@ import torch
 
 from tests import kv8_ref as ref
 from tests.helpers import say
-from tests.kv8_helpers import Case
+from tests.kv8_helpers import DTYPES, Case
 
 pytestmark = pytest.mark.gpu
 
@@ -59,3 +59,91 @@ def test_write_starts_in_no_order():
         torch.cuda.synchronize()
         for a, now in zip(was, cache_bytes(c)):
             assert torch.equal(a[free], now[free]), starts
+
+
+both = pytest.mark.parametrize("kernel", [1, 2])
+
+
+def largest_seen(c, n_q, window):
+    """The largest value that the finite scales of V which a row sees can stand for, [n_tok][n_q][1]."""
+    most = np.zeros((c.n_tok, n_q, 1))
+    for s, m in enumerate(c.lens):
+        scales = np.stack([np.repeat(c.vs[page], c.block, 1) for page in c.table[s, :-(-m // c.page)]], 1)
+        scales = np.where(np.isfinite(scales), scales, 0).reshape(c.hkv, -1)
+        for i in range(c.starts[s], c.starts[s + 1]):
+            pos = m - c.starts[s + 1] + i
+            seen = scales[:, max(0, pos - window + 1) if window else 0:pos + 1].max(1)
+            most[i, :, 0] = 127 * np.repeat(seen, n_q // c.hkv)
+    return most
+
+
+def check_by_row(c, q, q64, out, window, rows=None):
+    """As Case.check_attention, with the absolute part of each row's tolerance from the scales that the row sees: a
+    weight is rounded to fp16 in units in which the row's largest one is 2^7 at least and V's scale 2 at most, and
+    fp16 is off by 2^-25 at most below its normal numbers, so a key adds 2^-25 * 2 * vmax / 2^7 (also where
+    weights are in two halves, the second of which has the same least step)."""
+    scale = float(np.float32(1.0 / np.sqrt(c.d)))
+    want, _, mag, smag, keys = ref.attention(c.k, c.ks, c.v, c.vs, c.table, c.lens, c.starts, q64, scale, window)
+    halves = torch.float32 in (q.dtype, out.dtype)
+    vmax = largest_seen(c, q.shape[1], window)
+    tol = ref.attention_tolerance(want, mag, smag, keys, c.d, vmax, out.dtype, halves) + vmax * keys[..., None] * 2.0 ** -31
+    got = out.double().cpu().numpy()
+    if rows is not None:
+        got, want, tol = got[rows], want[rows], tol[rows]
+    assert np.array_equal(np.isnan(got), np.isnan(want)), "NaN at other places"
+    ok = ~np.isnan(want)
+    err = np.abs(got - want)[ok] / tol[ok]
+    say("worst", err.max())
+    assert err.max() <= 1, f"{(err > 1).sum()} of {err.size} outside, worst {err.max():.3g} times the tolerance"
+
+
+# a scale that a row does not see over those that it sees
+UNSEEN = [2.0 ** 12, 2.0 ** 25, 2.0 ** 60, 2.0 ** 125, np.nan, np.inf]
+
+
+@both
+@pytest.mark.parametrize("unseen", UNSEEN)
+@pytest.mark.parametrize("d,dtype", [(64, "bf16"), (64, "fp32"), (128, "bf16"), (128, "fp32"), (192, "bf16"), (256, "fp32"),
+                                     (512, "bf16")])
+@pytest.mark.parametrize("where", ["later", "before"])
+def test_scales_of_unseen_keys(where, d, dtype, unseen, kernel):
+    """Blocks that only later rows of the same tile see, or that lie before a row's window, have scales of V far
+    above those that the row sees, or none that is a number."""
+    say("unseen scales", where, d, dtype, unseen, kernel)
+    window = 20 if where == "before" else 0
+    c = Case([(40, 100), (9, 300), (33, 33), (5, 18)], 1, d, 64, 16, seed=d)
+    finite = np.isfinite(unseen)
+    c.ks[:], c.vs[:] = c.ks / 4, c.vs * np.float32(1.0 if finite else 2.0 ** -40)
+    sees = np.zeros(c.n_tok, bool)  # rows that have such a block among their keys
+    for s, (n, m) in enumerate(c.sizes):
+        blk = (m - 16) // 16 if where == "later" else max(m - n // 2 - window, 0) // 16
+        c.vs[c.table[s, blk // 4], 0, blk % 4] *= np.float32(unseen)
+        for i in range(n):
+            pos = m - n + i
+            lo = max(0, pos - window + 1) if window else 0
+            sees[c.starts[s] + i] = lo <= 16 * blk + 15 and pos >= 16 * blk
+    assert sees.any() and not sees.all()
+    c.upload()
+    q, q64 = c.rows(3, DTYPES[dtype])
+    lse = torch.empty(c.n_tok, 3, device="cuda")
+    out = c.q8.kv8_attention_debug(c.cache, c.batch, q, kernel, window=window, lse=lse)
+    torch.cuda.synchronize()
+    check_by_row(c, q, q64, out, window, None if not np.isinf(unseen) else ~sees)
+
+
+@both
+@pytest.mark.parametrize("dtype", ["bf16", "fp32"])
+@pytest.mark.parametrize("step", [2.0 ** 9, 2.0 ** 25, 2.0 ** -9, 2.0 ** -25])
+@pytest.mark.parametrize("window", [0, 20])
+def test_scales_that_grow_or_fall_by_block(window, step, dtype, kernel):
+    """Each block's scale of V is far from the last one's: every row has an exponent of its own."""
+    c = Case([(70, 90), (1, 90), (33, 60)], 1, 64, 16, 16, seed=41)
+    c.ks[:] /= 4
+    for s, (n, m) in enumerate(c.sizes):
+        for blk in range(-(-m // 16)):
+            c.vs[c.table[s, blk]] *= np.float32(step ** (blk - 2.5))
+    c.upload()
+    q, q64 = c.rows(3, DTYPES[dtype])
+    out = c.q8.kv8_attention_debug(c.cache, c.batch, q, kernel, window=window)
+    torch.cuda.synchronize()
+    check_by_row(c, q, q64, out, window)
