@@ -193,7 +193,9 @@ int run_attention(const kv8_cache *cache, const kv8_batch *batch, const kv8_atte
       (splits > 1 && (int64_t)b.n_tok * x.n_q > kv::kMaxJoinRows))
     return Q8_0_EINVAL;
   if (nothing_to_do(b)) return Q8_0_OK;
-  kv::Attention a{x.out, {}, x.out_type, x.n_q, x.n_q / c.n_kv, x.window, x.scale, x.sinks, x.lse};
+  // a window of all positions is none (and a position below 0 less a larger one would leave 32 bits)
+  const int32_t window = x.window < kMaxLen ? x.window : 0;
+  kv::Attention a{x.out, {}, x.out_type, x.n_q, x.n_q / c.n_kv, window, x.scale, x.sinks, x.lse};
   if ((st = check_pointers(c, b)) != Q8_0_OK || (st = read_rows(x.q, x.q_token_stride, x.q_head_stride, x.q_type, &a.q)) != Q8_0_OK)
     return st;
   if (!x.out) return Q8_0_EINVAL;
@@ -201,7 +203,7 @@ int run_attention(const kv8_cache *cache, const kv8_batch *batch, const kv8_atte
   if (!workspace) workspace_bytes = 0;
   kv::Plan p{kernel == KV8_KERNEL_TILED, splits > 1 ? splits : 1};
   if (kernel == KV8_KERNEL_AUTO)
-    p = kv::attention_plan(c, b, x.n_q, x.window, halves, workspace_bytes);
+    p = kv::attention_plan(c, b, x.n_q, window, halves, workspace_bytes);
   else if (kv::partial_bytes(c, b, x.n_q, p.splits) > workspace_bytes)
     return Q8_0_EWORKSPACE;
   if ((st = q8::check_device()) != Q8_0_OK) return st;

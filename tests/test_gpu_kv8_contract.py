@@ -147,3 +147,17 @@ def test_scales_that_grow_or_fall_by_block(window, step, dtype, kernel):
     out = c.q8.kv8_attention_debug(c.cache, c.batch, q, kernel, window=window)
     torch.cuda.synchronize()
     check_by_row(c, q, q64, out, window)
+
+
+@both
+@pytest.mark.parametrize("window", [2 ** 31 - 1, 2 ** 30, 2 ** 30 - 1])
+def test_windows_beyond_every_length(window, kernel):
+    """A window that no length reaches is none, also in tiles that begin at positions below 0."""
+    c = Case([(20, 7), (1, 40), (300, 290), (5, 0)], 1, 64, seed=43).upload()
+    q, q64 = c.rows(1, torch.bfloat16)
+    lse, lse0 = (torch.empty(c.n_tok, 1, device="cuda") for _ in range(2))
+    out = c.q8.kv8_attention_debug(c.cache, c.batch, q, kernel, window=window, lse=lse)
+    assert torch.equal(out, c.q8.kv8_attention_debug(c.cache, c.batch, q, kernel, lse=lse0)) and torch.equal(lse, lse0)
+    c.check_attention(q, q64, out, lse)
+    auto = c.q8.kv8_attention(c.cache, c.batch, q, window=window)
+    assert torch.equal(auto, c.q8.kv8_attention(c.cache, c.batch, q))
