@@ -124,8 +124,9 @@ size_t kv8_attention_workspace_bytes(const kv8_cache *cache, const kv8_batch *ba
  * A row without keys (a position below 0, a sequence of length 0) gives zeros and
  * lse = sink or -infinity.  Keys that a row does not see have no part in it,
  * whatever their scales hold.  Rows behind the last sequence are left as they were.
- * A NaN scale makes the rows that see its tokens NaN, and so does a page id out of
- * 0 .. n_pages - 1.  A NaN or an infinity in a query makes that row NaN.
+ * A NaN scale makes the rows that see its tokens NaN (one of V not their lse, which has
+ * no V in it), and so does a page id out of 0 .. n_pages - 1.  A NaN or an infinity in a
+ * query makes that row NaN.
  * Numbers: codes enter the matrix core exactly as fp16, queries as fp16 under a
  * power of two per row (16-bit queries exactly, but for values below 2^-28 of the
  * row's largest), fp32 queries as two such halves; exp, sums and outputs are fp32.

@@ -305,6 +305,7 @@ __global__ __launch_bounds__((Shape<D, HALVES>::kThreads), (Shape<D, HALVES>::kW
   // A tile's scores on their way to weights: log2 of the weights times V's scale over 2^e, and what
   // a group's sum of them is multiplied with.
   float y[kSubs][16], share[kGroups];
+  bool summed;  // l has the tile's weights already, from its scores alone
   auto weights = [&](h8 (&ph)[kGroups], h8 (&pl)[kGroups], float &add) {
     float sum[kGroups];
 #pragma unroll
@@ -353,7 +354,7 @@ __global__ __launch_bounds__((Shape<D, HALVES>::kThreads), (Shape<D, HALVES>::kW
       raise();
       weights(ph, pl, add);
     }
-    l += add;
+    l += summed ? 0.f : add;  // (add is NaN where a scale of V is)
   };
   // y of tile t from its products, before the rare cases below
   float fk[kGroups], lw[kGroups];
@@ -367,6 +368,7 @@ __global__ __launch_bounds__((Shape<D, HALVES>::kThreads), (Shape<D, HALVES>::kW
     const int most = __builtin_amdgcn_readfirstlane(of_tile[0]);
     least = __builtin_amdgcn_readfirstlane(of_tile[1]);
     e_next = max(e, most);
+    summed = false;
     odd = unset || most > e_low || least < e_high - kFoldBits;
     const float shift = (float)(most - e_next), back = ldexp_fast(1.f, e_next - most);
 #pragma unroll
@@ -430,8 +432,8 @@ __global__ __launch_bounds__((Shape<D, HALVES>::kThreads), (Shape<D, HALVES>::kW
       scale_sums(ldexp_fast(1.f, e - e_next));
       e = e_next;
     }
-    const bool unfolded = __any(low < e - kFoldBits);
-    if (unfolded || __any(m == kLowest)) {
+    summed = __any(low < e - kFoldBits);
+    if (summed || __any(m == kLowest)) {
       float top = kLowest;
 #pragma unroll
       for (int sub = 0; sub < kSubs; ++sub)
@@ -453,13 +455,9 @@ __global__ __launch_bounds__((Shape<D, HALVES>::kThreads), (Shape<D, HALVES>::kW
 #pragma unroll
         for (int j = 0; j < 16; ++j) {
           const float x = y[sub][j] - mb;
-          if (unfolded) l += exp2_fast(x);
+          if (summed) l += exp2_fast(x);
           y[sub][j] = x == -INFINITY ? x : x + lw[2 * sub + (j >> 3)];
         }
-      if (unfolded) {
-#pragma unroll
-        for (int i = 0; i < kGroups; ++i) share[i] = 0.f;
-      }
     }
     unset = __any(m == kLowest);
     e_low = e_high = __builtin_amdgcn_readfirstlane(e);

@@ -161,3 +161,26 @@ def test_windows_beyond_every_length(window, kernel):
     c.check_attention(q, q64, out, lse)
     auto = c.q8.kv8_attention(c.cache, c.batch, q, window=window)
     assert torch.equal(auto, c.q8.kv8_attention(c.cache, c.batch, q))
+
+
+@both
+@pytest.mark.parametrize("splits", [1, 3])
+@pytest.mark.parametrize("dtype", ["bf16", "fp32"])
+@pytest.mark.parametrize("d", [64, 128, 256])
+def test_lse_does_not_depend_on_values(d, dtype, splits, kernel):
+    """A row that sees a NaN scale of V is NaN, and its log sum is that of its scores; a NaN scale of K makes both NaN."""
+    c = Case([(1, 100), (90, 100), (3, 50), (1, 700), (40, 40)], 1, d, 16, 16, seed=44)
+    c.vs[c.table[1, 3]] = np.nan   # tokens 48 .. 63
+    c.vs[c.table[2, 2]] = np.nan   # tokens 32 .. 47
+    c.vs[c.table[3, 20]] = 0.0
+    c.vs[c.table[4, 0]] = np.nan
+    c.ks[c.table[4, 1]] = np.nan
+    c.upload()
+    q, q64 = c.rows(3, DTYPES[dtype])
+    lse = torch.empty(c.n_tok, 3, device="cuda")
+    out = c.q8.kv8_attention_debug(c.cache, c.batch, q, kernel, splits=splits, lse=lse)
+    torch.cuda.synchronize()
+    c.check_attention(q, q64, out, lse)
+    whole, sums = out.isnan().all(-1).all(-1).cpu(), lse.isnan().all(-1).cpu()
+    assert whole[39:94].all() and not sums[39:94].any() and not whole[:39].any() and not whole[94]
+    assert whole[95:].all() and not sums[95:111].any() and sums[111:].all()
