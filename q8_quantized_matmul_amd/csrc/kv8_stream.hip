@@ -268,7 +268,8 @@ __global__ __launch_bounds__(256) void stream_kernel(Cache c, Batch b, Attention
 // out[row] = sum over splits of out_s * exp2(lse2_s) / (their sum, and the sink's).  A thread takes 4 dims.  Up to
 // kFewSplits a workgroup takes as many rows as fit, a thread all splits of its row; above, one row, of which a thread
 // has every n-th split (what bounds it is latency: a row's loads are on their way together), and the n
-// sums are added in order.
+// sums are added in order.  Every split has written every row (zeros where it has no key of it), so weights that
+// vanish multiply too: a row that sees a NaN keeps it.
 constexpr int kMostSplits = 256, kFewSplits = 8;
 __global__ __launch_bounds__(256) void join_kernel(Cache c, Batch b, Attention a, int splits, const void *ws) {
   __shared__ float weight[kMostSplits], wave_top[4], wave_sum[4];
@@ -300,7 +301,7 @@ __global__ __launch_bounds__(256) void join_kernel(Cache c, Batch b, Attention a
       const float w = z[s] == -INFINITY ? 0.f : exp2_fast(z[s] - top);
       sum += w;
 #pragma unroll
-      for (int j = 0; j < 4; ++j) v[j] += w == 0.f ? 0.f : y[s][j] * w;  // (nothing was written where it is 0)
+      for (int j = 0; j < 4; ++j) v[j] += s < splits ? y[s][j] * w : 0.f;
     }
   } else {
     const float z = tid < splits ? part.lse2[tid * part.rows + row] : -INFINITY;
@@ -324,7 +325,7 @@ __global__ __launch_bounds__(256) void join_kernel(Cache c, Batch b, Attention a
         const float f = weight[s];
         const f32x4 y = *reinterpret_cast<const f32x4 *>(x + s * stride);
 #pragma unroll
-        for (int j = 0; j < 4; ++j) v[j] += f == 0.f ? 0.f : y[j] * f;
+        for (int j = 0; j < 4; ++j) v[j] += y[j] * f;
       }
     }
     sums[tid] = v;

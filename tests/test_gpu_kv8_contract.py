@@ -184,3 +184,28 @@ def test_lse_does_not_depend_on_values(d, dtype, splits, kernel):
     whole, sums = out.isnan().all(-1).all(-1).cpu(), lse.isnan().all(-1).cpu()
     assert whole[39:94].all() and not sums[39:94].any() and not whole[:39].any() and not whole[94]
     assert whole[95:].all() and not sums[95:111].any() and sums[111:].all()
+
+
+@both
+@pytest.mark.parametrize("splits", [1, 2, 5, 8, 9, 40])
+@pytest.mark.parametrize("far", [10.0, 3000.0])
+def test_nan_values_of_vanishing_weight(far, splits, kernel):
+    """A NaN scale of V under keys whose weights vanish in fp32: the rows that see it are NaN, whichever split it falls
+    in; zero weights of other blocks add nothing."""
+    c = Case([(1, 1300), (3, 1300), (2, 1300)], 1, 64, 16, 16, seed=45)
+    c.k[..., 0] = 100
+    for s in range(3):
+        c.ks[c.table[s, 70:82]] *= np.float32(far)  # tokens from 1120 on: scores far above the others
+    c.vs[c.table[0, 3]] = np.nan
+    c.vs[c.table[2, 60]] = np.nan
+    c.upload()
+    q, _ = c.rows(2, torch.float32)
+    q = q.abs()
+    lse = torch.empty(c.n_tok, 2, device="cuda")
+    out = c.q8.kv8_attention_debug(c.cache, c.batch, q, kernel, splits=splits, lse=lse, scale=1.0)
+    torch.cuda.synchronize()
+    rows = out.isnan().all(-1).all(-1).tolist()
+    assert rows == [True, False, False, False, True, True] and out.isnan().any(-1).any(-1).tolist() == rows
+    assert lse.isfinite().all()
+    if far < 100:
+        c.check_attention(q, q.double().cpu().numpy(), out, lse, scale=1.0)
