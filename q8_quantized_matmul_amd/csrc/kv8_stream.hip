@@ -160,7 +160,7 @@ __global__ __launch_bounds__(256) void stream_kernel(Cache c, Batch b, Attention
         top = fmaxf(top, __shfl_xor(top, 16));
         top = fmaxf(top, __shfl_xor(top, 32));
         const float was = m;
-        m = fmaxf(m, top);
+        m = top > m + kSlack ? top : m;  // by row: no other row's keys move its bound
         const float f = exp2_fast(was - m);
         l *= f;
 #pragma unroll

@@ -305,7 +305,7 @@ __global__ __launch_bounds__((Shape<D, HALVES>::kThreads), (Shape<D, HALVES>::kW
   // A tile's scores on their way to weights: log2 of the weights times V's scale over 2^e, and what
   // a group's sum of them is multiplied with.
   float y[kSubs][16], share[kGroups];
-  bool summed;  // l has the tile's weights already, from its scores alone
+  bool summed;  // by row: l has the tile's weights already, from its scores alone
   auto weights = [&](h8 (&ph)[kGroups], h8 (&pl)[kGroups], float &add) {
     float sum[kGroups];
 #pragma unroll
@@ -329,15 +329,16 @@ __global__ __launch_bounds__((Shape<D, HALVES>::kThreads), (Shape<D, HALVES>::kW
     }
     return most;
   };
-  // A row's weights are too large for fp16: its bound moves up to its largest score.
-  auto raise = [&] {
+  // Some row's weights are too large for fp16: its bound moves up to its largest score, the others' stay.
+  auto raise = [&](float most) {
+    const bool mine = fmaxf(most, __shfl_xor(most, 32)) > kMostSum;
     float top = y[0][0];
 #pragma unroll
     for (int sub = 0; sub < kSubs; ++sub)
 #pragma unroll
       for (int j = 0; j < 16; ++j) top = fmaxf(top, y[sub][j]);
     top = fmaxf(top, __shfl_xor(top, 32));
-    const float by = fmaxf(top - kBias, 0.f);
+    const float by = mine ? fmaxf(top - kBias, 0.f) : 0.f;
     m += by;
     const float f = exp2_fast(-by);
     l *= f;
@@ -349,9 +350,10 @@ __global__ __launch_bounds__((Shape<D, HALVES>::kThreads), (Shape<D, HALVES>::kW
   };
   auto all_weights = [&](h8 (&ph)[kGroups], h8 (&pl)[kGroups]) {
     float add;
-    if (__any(weights(ph, pl, add) > kMostSum)) {
+    const float most = weights(ph, pl, add);
+    if (__any(most > kMostSum)) {
       rare();
-      raise();
+      raise(most);
       weights(ph, pl, add);
     }
     l += summed ? 0.f : add;  // (add is NaN where a scale of V is)
@@ -432,32 +434,35 @@ __global__ __launch_bounds__((Shape<D, HALVES>::kThreads), (Shape<D, HALVES>::kW
       scale_sums(ldexp_fast(1.f, e - e_next));
       e = e_next;
     }
-    summed = __any(low < e - kFoldBits);
-    if (summed || __any(m == kLowest)) {
+    summed = low < e - kFoldBits;
+    const bool anew = summed || m == kLowest;
+    if (__any(anew)) {
       float top = kLowest;
 #pragma unroll
       for (int sub = 0; sub < kSubs; ++sub)
 #pragma unroll
         for (int j = 0; j < 16; ++j) {
-          const float x = __builtin_fmaf(z[sub][j], fk[2 * sub + (j >> 3)], 0.f);
-          y[sub][j] = unseen(pos, sub, j) ? -INFINITY : x;
+          y[sub][j] = unseen(pos, sub, j) ? -INFINITY : z[sub][j] * fk[2 * sub + (j >> 3)];
           top = fmaxf(top, y[sub][j]);
         }
       top = fmaxf(top, __shfl_xor(top, 32));
       const float was = m;
-      m = fmaxf(m, top);
+      m = anew ? fmaxf(m, top) : m;
       const float f = exp2_fast(was - m);
       l *= f;
       scale_sums(f);
       const float mb = m - kBias;
+      float sum = 0.f;
 #pragma unroll
       for (int sub = 0; sub < kSubs; ++sub)
 #pragma unroll
         for (int j = 0; j < 16; ++j) {
-          const float x = y[sub][j] - mb;
-          if (summed) l += exp2_fast(x);
-          y[sub][j] = x == -INFINITY ? x : x + lw[2 * sub + (j >> 3)];
+          // of a row's largest score nothing is left by the first of these but kBias; the other rows' are as they were
+          const float x = y[sub][j] - mb, as_was = __builtin_fmaf(z[sub][j], fk[2 * sub + (j >> 3)], lw[2 * sub + (j >> 3)] - mb);
+          sum += exp2_fast(x);
+          y[sub][j] = x == -INFINITY ? x : anew ? x + lw[2 * sub + (j >> 3)] : as_was;
         }
+      l += summed ? sum : 0.f;
     }
     unset = __any(m == kLowest);
     e_low = e_high = __builtin_amdgcn_readfirstlane(e);

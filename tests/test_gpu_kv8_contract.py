@@ -209,3 +209,55 @@ def test_nan_values_of_vanishing_weight(far, splits, kernel):
     assert lse.isfinite().all()
     if far < 100:
         c.check_attention(q, q.double().cpu().numpy(), out, lse, scale=1.0)
+
+
+@both
+@pytest.mark.parametrize("splits", [1, 3])
+@pytest.mark.parametrize("d,dtype", [(64, "bf16"), (64, "fp32"), (128, "bf16"), (128, "fp32"), (192, "bf16"), (256, "bf16"), (512, "bf16")])
+def test_unseen_keys_change_no_bit(d, dtype, splits, kernel):
+    """Other tokens behind a row, or before its window, whatever they hold, leave its output's and log sum's bits:
+    rows of one tile have bounds and exponents of their own."""
+    c = Case([(40, 100), (70, 300), (33, 33), (3, 290), (40, 340)], 1, d, 64, 16, seed=46)
+    c.ks[:] /= 4
+    q = None
+    border = [80, 256, 16, 288, 304]  # tokens from here on change
+    kept = [(k.copy(), v.copy()) for k, v in ((c.k, c.ks), (c.v, c.vs))]
+    for window in (0, 20):
+        before = window > 0  # those before the border change
+        want = None
+        for what in range(7):
+            for (codes, scales), (k0, s0), which in (((c.k, c.ks), kept[0], "k"), ((c.v, c.vs), kept[1], "v")):
+                codes[:], scales[:] = k0, s0
+                for s, (n, m) in enumerate(c.sizes):
+                    for blk in (range(border[s] // 16) if before else range(border[s] // 16, -(-m // 16))):
+                        at = (c.table[s, blk // 4], 0, blk % 4)
+                        if what == 1:
+                            scales[at] *= np.float32(60.0) if which == "k" else np.float32(1.0)  # scores far above
+                        elif what == 2:
+                            scales[at] *= np.float32(2.0 ** 100) if which == "v" else np.float32(1.0)
+                        elif what == 3:
+                            scales[at] = 0
+                        elif what == 4:
+                            scales[at] = np.nan
+                        elif what == 5:
+                            scales[at] *= np.float32(2.0 ** -30)
+                        elif what == 6:
+                            page = codes[at[0], 0, 16 * at[2]:16 * at[2] + 16]
+                            page[:] = c.rng.integers(-127, 128, page.shape)
+            c.upload()
+            if q is None:
+                q, _ = c.rows(3, DTYPES[dtype], spread=2.0)
+            lse = torch.empty(c.n_tok, 3, device="cuda")
+            out = c.q8.kv8_attention_debug(c.cache, c.batch, q, kernel, splits=splits, window=window, lse=lse)
+            torch.cuda.synchronize()
+            rows = []
+            for s, (n, m) in enumerate(c.sizes):
+                pos = np.arange(m - n, m)
+                rows.append(pos - window + 1 >= border[s] if before else pos < border[s])
+            rows = torch.from_numpy(np.concatenate(rows)).cuda()
+            assert rows.any() and not rows.all()
+            got = out[rows], lse[rows]
+            assert got[0].isfinite().all() and got[1].isfinite().all()
+            if want is None:
+                want = got
+            assert torch.equal(got[0], want[0]) and torch.equal(got[1], want[1]), (window, what)
