@@ -43,7 +43,7 @@ enum { KV8_F32 = 0, KV8_BF16 = 1, KV8_F16 = 2 };
 typedef struct kv8_cache {
     void *k_codes, *v_codes;
     float *k_scales, *v_scales; /* not negative, as kv8_write makes them             */
-    int64_t n_pages;    /* 0 .. 2^31 - 1                                            */
+    int64_t n_pages;    /* 1 .. 2^31 - 1                                            */
     int32_t n_kv;       /* key/value heads, 1 .. 4096                               */
     int32_t head_dim;   /* 64, 128, 192, 256 or 512                                 */
     int32_t page_size;  /* tokens of a page: a power of two, 16 .. 1024             */
@@ -61,7 +61,7 @@ typedef struct kv8_batch {
     const int32_t *page_table;  /* int32 [n_seq][table_width]                        */
     const int32_t *lens;        /* int32 [n_seq]                                     */
     const int32_t *starts;      /* int32 [n_seq + 1], ascending from 0; NULL: one row each */
-    int64_t n_seq;              /* 0 .. 2^20                                         */
+    int64_t n_seq;              /* 0 .. 2^20, and n_seq * n_kv <= 2^22               */
     int64_t n_tok;              /* rows of the token arrays, 0 .. 2^24; n_seq where starts is NULL */
     int64_t table_width;        /* pages of a table row; table_width * page_size <= 2^30 */
     int64_t max_new;            /* no sequence may have more rows than this (1 where starts is NULL) */
@@ -104,15 +104,15 @@ typedef struct kv8_attention_args {
     const void *q;         /* [n_tok][n_q][head_dim] of q_type                               */
     int64_t q_token_stride, q_head_stride; /* in elements, as k's of kv8_write               */
     int32_t out_type, q_type;
-    int32_t n_q;           /* query heads, a multiple of n_kv, up to 2^14; head h reads key/value head h / (n_q / n_kv) */
+    int32_t n_q;           /* query heads, a multiple of n_kv, up to 2^14, and n_tok * n_q <= 2^27; head h reads key/value head h / (n_q / n_kv) */
     int32_t window;        /* keys a row sees, its own among them; 0: all before it          */
     float scale;           /* on the scores, e.g. 1 / sqrt(head_dim)                         */
     const float *sinks;    /* optional fp32 [n_q]: a score without a value, per head         */
     float *lse;            /* optional fp32 [n_tok][n_q], written                            */
 } kv8_attention_args;
 
-/* Workspace bytes of kv8_attention's fastest plan (partial outputs of a split
- * over the keys); 0 when it needs none or the arguments are invalid. */
+/* Workspace bytes of kv8_attention's fastest plan without a window (partial outputs of a
+ * split over the keys); 0 when it needs none or the arguments are invalid. */
 size_t kv8_attention_workspace_bytes(const kv8_cache *cache, const kv8_batch *batch, int32_t n_q);
 
 /* Causal attention of the batch's rows over their sequences' cached tokens (the

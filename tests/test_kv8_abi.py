@@ -153,3 +153,16 @@ def test_binding_refuses_host_tensors(q8):
         q8.Kv8Batch(torch.zeros(1, 1, dtype=torch.int32), torch.zeros(1, dtype=torch.int32))
     with pytest.raises(ValueError, match="multiple of block"):
         q8.kv8_cache(1, 1, 64, page_size=64, block=24, device="cpu")
+
+
+def test_stated_limits(q8, calls):
+    """The header's limits of products of sizes: at them a call is looked at further (and refused for its alignment),
+    above them refused."""
+    wide = dict(batch=dict(n_seq=1, n_tok=1 << 20, max_new=1 << 20), cache=dict(n_kv=1))
+    assert calls["attention"](n_q=128, out=FAKE + 8, **wide) == q8.Q8_0_EALIGN
+    assert calls["attention"](n_q=129, out=FAKE + 8, **wide) == q8.Q8_0_EINVAL
+    for call in ("write", "read"):
+        assert calls[call](cache=dict(n_kv=4, k_codes=FAKE + 8), batch=dict(n_seq=1 << 20)) == q8.Q8_0_EALIGN
+        assert calls[call](cache=dict(n_kv=5, k_codes=FAKE + 8), batch=dict(n_seq=1 << 20)) == q8.Q8_0_EINVAL
+    assert calls["read"](cache=dict(n_pages=1, k_codes=FAKE + 8)) == q8.Q8_0_EALIGN
+    assert calls["read"](cache=dict(n_pages=0, k_codes=FAKE + 8)) == q8.Q8_0_EINVAL
