@@ -253,7 +253,9 @@ __global__ __launch_bounds__((Shape<D, HALVES>::kThreads), (Shape<D, HALVES>::kW
   for (int i = 0; i < kDimTiles; ++i)
 #pragma unroll
     for (int j = 0; j < 16; ++j) o[i][j] = 0.f;
-  float m = kLowest, l = 0.f;
+  // (rows behind a sequence's last are given a bound that nothing reaches: without one they would take their wave into
+  // the rare branch in every tile)
+  float m = row_ok ? kLowest : -kLowest, l = 0.f;
   int e = kNoScale;
   auto scale_sums = [&](float f) {
 #pragma unroll
