@@ -91,13 +91,13 @@ size_t partial_bytes(const Cache &c, const Batch &b, int n_q, int splits) {
 //     gives one every `shared` where it has several;
 //   tiled: a unit takes `tile` for `keys` keys of all its rows, `at_once` workgroups beside each other.
 // Both take some us before the first key and behind the last, the join of splits some more, and its traffic.
-// What the estimates decide, measured (us, stream / tiled): heads of 128, 8 of them, groups of 4: 256 tokens
-// 9 / 19; 2 x 1000 tokens 69 / 58; 40 sequences of 32 tokens over 2000 keys 123 / 178; 8192 tokens
-// 1368 / 610.  Heads of 512, 64 on one, 2 x 300 tokens over 4000 keys 946 / 808; 12 single tokens over up
-// to 6000 keys 57 / 78.  Splits of the stream kernel, one sequence of 2000 keys, 1 / 4 / 16: 20 / 12 / 10; of
-// 131072 keys, 16 / 64: 82 / 48; of 64 sequences of up to 8192, 1 / 4: 133 / 137.  Splits of the tiled kernel,
-// 512 tokens over 32768 keys, 1 / 2 / 4 / 8: 883 / 457 / 285 / 303 (stream, at its best, 668); 2048 over
-// 16384, 1 / 2: 526 / 538.
+// What the estimates decide, measured (us, whole calls, stream / tiled): heads of 128, 8 of them, groups of 4: 256
+// tokens 10 / 21; 2 x 1000 tokens 75 / 46; 40 sequences of 32 tokens over 2000 keys 133 / 146; 8192 tokens
+// 1369 / 562.  Heads of 512, 64 on one, 2 x 300 tokens over 4000 keys 956 / 798; 12 single tokens over up
+// to 6000 keys in four and eight splits 58 / 75.  Splits of the stream kernel, one sequence of 2000 keys, 1 / 4 / 16:
+// 21 / 13 / 11; of 131072 keys, 16 / 64: 99 / 59; of 64 sequences of up to 8192, 1 / 4: 135 / 140.  Splits of the
+// tiled kernel, 512 tokens over 32768 keys, 1 / 2 / 4 / 8: 900 / 467 / 284 / 300 (stream, without splits, 715); 2048
+// over 16384, 1 / 2: 515 / 524.
 struct Cost {
   float alone, shared, tile;
   int keys, at_once;

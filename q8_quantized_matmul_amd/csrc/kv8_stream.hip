@@ -11,8 +11,9 @@
 // What bounds it is HBM: 2 * d bytes a key, 160 VALU instructions a lane for the codes of 32 keys
 // of 128 values (8 KB) beside 16 matrix instructions.  Measured, 32 heads of 128 on 8: 64 sequences of up to
 // 8192 tokens (667 MB) 133 us, 5.0 TB/s, a copy of 1 GiB reaching 5.1; one of 131072 (269 MB) 57 us and 5
-// for the join; one of 2000 6.4 us and 4 to 5.  64 heads of 512 on one, 12 sequences of up to 6000: 52 us, bound by the
-// conversion of the codes, which each of the four tiles of 16 rows repeats.  Not taken: the next step's codes fetched
+// for the join; one of 2000 6.4 us and 4 to 5.  64 heads of 512 on one, 12 sequences of up to 6000: 52 us, where
+// each of the four tiles of 16 rows loads and converts the codes again (178 MB for 45) and, at one wave a SIMD, waits for
+// its loads with nothing else to do: the vector ALU is busy for 26 %.  Not taken: the next step's codes fetched
 // behind this step's products (8 % slower for 131072 tokens: fewer waves fit); two tiles of rows a wave,
 // two waves sharing the dims of a head of 512 (10 % faster there, elsewhere slower).
 #include "kv8_attn.h"

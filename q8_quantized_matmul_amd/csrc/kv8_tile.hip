@@ -17,8 +17,10 @@
 // a tile ahead of V; each has two buffers, and there is one barrier a step.
 //
 // Measured, causal, 32 heads of 128 on 8, bf16: 8192 tokens 560 to 610 us (900 to 980 TFLOP/s of the live half), 32768
-// tokens 8.4 to 8.7 ms (1.0 PFLOP/s); torch's product of two fp16 matrices of 8192 reaches 1.17 on the same card.
-// Both run at about 2.0 GHz.  512 tokens over 32768 keys, split in four, 288 us (957 TFLOP/s).  On the way there (8192 tokens): weights, then products, tile by tile 806 us; page ids
+// tokens 8.2 to 8.5 ms (1.0 PFLOP/s); torch's product of two fp16 matrices of 8192 reaches 1.17 on the same card.
+// Both run at about 2.0 GHz.  512 tokens over 32768 keys, split in four, 284 to 300 us.  8192 tokens
+// of heads of 64 404 to 441 us (640 TFLOP/s), of 192 1660 (495), of 256 1820 (600): those of 192 and 256 hold four waves
+// and tiles of 32 keys.  On the way there (8192 tokens): weights, then products, tile by tile 806 us; page ids
 // looked up a tile ahead of the codes, which nothing then waits for, 647; both at once 617.  Not taken, all within 5 %
 // of it or slower: deeper operand reads, a fixed order of products and vector work with scores of two tiles in
 // registers (their spills wait for the loads in flight), sums by dot products (they run on the matrix core), four
@@ -459,7 +461,8 @@ __global__ __launch_bounds__((Shape<D, HALVES>::kThreads), (Shape<D, HALVES>::kW
       for (int sub = 0; sub < kSubs; ++sub)
 #pragma unroll
         for (int j = 0; j < 16; ++j) {
-          // of a row's largest score nothing is left by the first of these but kBias; the other rows' are as they were
+          // x: for a row's largest score kBias to the bit, however large (one rounding, as in scale_scores, would
+          // leave that score's last bits); rows with a bound keep what they had
           const float x = y[sub][j] - mb, as_was = __builtin_fmaf(z[sub][j], fk[2 * sub + (j >> 3)], lw[2 * sub + (j >> 3)] - mb);
           sum += exp2_fast(x);
           y[sub][j] = x == -INFINITY ? x : anew ? x + lw[2 * sub + (j >> 3)] : as_was;

@@ -2,9 +2,10 @@
 //
 // A wave takes 16 tokens of one head, keys or values: the granule in which both
 // code layouts are contiguous (16 * d bytes).  The waves of one block of tokens
-// sit in one workgroup, so the block's scale is one LDS exchange away.  Both
-// kernels are bound by HBM for prompts (2 + 1 bytes a 16-bit value) and by the
-// chain table -> scale and codes -> store for single tokens.
+// sit in one workgroup, so the block's scale is one LDS exchange away.  For
+// single tokens both kernels are bound by the chain table -> scale and codes -> store, for
+// prompts (2 + 1 bytes a 16-bit value) reading by HBM (16384 tokens of 8 heads of 128 18.5 us, 5.4 TB/s),
+// writing at 2.7 TB/s (36.8 us) by one round trip a wave and the exact quotients.
 #include "kv8_device.h"
 
 namespace kv {
