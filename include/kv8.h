@@ -76,7 +76,8 @@ typedef struct kv8_batch {
  * Per block and head, N being its new rows and O its tokens before the first of
  * them:
  *   s1 = max(|N|) / 127 in fp32, or the old scale where O is not empty and that is larger
- *   new codes = N / s1 rounded to nearest even (the exact quotient; 0 where s1 is 0),
+ *   new codes = N / s1 rounded to nearest even (the exact quotient, held within -127 .. 127,
+ *   which subnormal scales alone exceed; 0 where s1 is 0),
  *   O's codes = code * s0 / s1 rounded to nearest even, where the scale grew from s0.
  * A NaN or an infinity in N, or a NaN scale of O, gives s1 = NaN and new codes 0.
  * Codes are bit-exact for every input.  Tokens of the block behind the new ones
